@@ -2,7 +2,8 @@
  * dg.h -- C ABI of the MI355X (gfx950) FP8 block-scaled GEMM library: the
  * NT GEMM and its M-grouped MoE forms, the E4M3 quantisers, the NN/TN/TT
  * layouts, the K-grouped weight-gradient GEMM, power-of-two (UE8M0) scale
- * variants, and the FP8 MQA logits.
+ * variants, the FP8 MQA logits, and the operators around the GEMMs of a
+ * gated feed-forward layer (norm, gating and their gradients).
  *
  * Operation (the "DeepGEMM" README summary on GeekNews, ja.news.hada.io topic
  * 19459, section "GEMM interface and layout constraints"): D = C + A . B^T in
@@ -421,6 +422,184 @@ int dg_k_grouped_fp8_gemm_tn_contiguous(const uint8_t *a, const float *sfa,
                                         const uint8_t *b, const float *sfb,
                                         const int32_t *ks, const float *c, float *d,
                                         int M, int N, int K, int G, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The feed-forward layer around the GEMMs: the norm that makes the first
+ * GEMM's operand, the gated projections that make the second's, and the
+ * gradients of both.  Conventions as above, except that
+ *  - a call with no rows (rows, M or M_total = 0) is valid: it writes nothing
+ *    (dg_rmsnorm_backward: dw = 0) and returns DG_OK; pointers may be NULL then;
+ *  - outputs marked optional may be NULL and are then not computed;
+ *  - tensors whose element type varies are void pointers with a dg_type.
+ * Statistics, activations and maxima are computed in fp32; every output is
+ * rounded once, from fp32.  NaN and infinities follow the formulas in fp32;
+ * in the quantised outputs they are treated as by the quantisers above.
+ * ------------------------------------------------------------------------ */
+typedef enum dg_type { DG_BF16 = 0, DG_F32 = 1 } dg_type;
+typedef enum dg_act {
+    DG_ACT_SILU = 0,      /* g / (1 + exp(-g)) */
+    DG_ACT_GELU_TANH = 1  /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+} dg_act;
+
+/*
+ * Residual addition, RMS norm and 1x128 E4M3 quantisation in one pass:
+ *   h = x + residual;  y = h / sqrt(mean_k(h^2) + eps) * weight
+ *   q, sf = the 1x128 quantiser's output on y (before any rounding of y)
+ *   x [rows][ld_x >= K]        DG_BF16 or DG_F32; the row pitch lets the norm
+ *                              read a column range of a wider matrix
+ *   residual [rows][K]         or NULL (= 0); its type is also residual_out's
+ *   weight [K]                 DG_BF16 or DG_F32
+ *   residual_out [rows][K]     optional: h, rounded to its type; may be the
+ *                              residual itself (in place).  The norm uses h
+ *                              before that rounding.
+ *   y [rows][K] bf16           optional
+ *   q [rows][K] E4M3, sf       optional (q and sf together; y or q is needed)
+ * The scales are those of dg_quantize_e4m3_1x128 (sf [K/128][ld_sf] fp32), of
+ * its _ue8m0 form, or (_ue8m0_packed) the packed words of the latter,
+ * sf [ceil(K/512)][ld_sf] with the unused high bytes zero; entries of rows
+ * past the last are not written.
+ * Sums of squares overflow fp32 for |h| above about 1e19: mean(h^2) is then
+ * infinite and y zero.
+ * Errors: DG_ERR_NULL; DG_ERR_SHAPE (rows < 0; K < 128, K % 128, K > 16384);
+ * DG_ERR_ARG (a type; eps negative or NaN; residual_out without residual);
+ * DG_ERR_ALIGN (a pointer not 16-byte aligned; ld_x < K or its rows not
+ * 16-byte aligned; ld_sf < rows or ld_sf % 4).
+ */
+int dg_rmsnorm_quantize_e4m3_1x128(const void *x, int x_type, int64_t ld_x,
+                                   const void *residual, int residual_type,
+                                   const void *weight, int weight_type, float eps,
+                                   void *residual_out, uint16_t *y,
+                                   uint8_t *q, float *sf, int ld_sf,
+                                   int rows, int K, void *stream);
+int dg_rmsnorm_quantize_e4m3_1x128_ue8m0(const void *x, int x_type, int64_t ld_x,
+                                         const void *residual, int residual_type,
+                                         const void *weight, int weight_type, float eps,
+                                         void *residual_out, uint16_t *y,
+                                         uint8_t *q, float *sf, int ld_sf,
+                                         int rows, int K, void *stream);
+int dg_rmsnorm_quantize_e4m3_1x128_ue8m0_packed(const void *x, int x_type, int64_t ld_x,
+                                                const void *residual, int residual_type,
+                                                const void *weight, int weight_type, float eps,
+                                                void *residual_out, uint16_t *y,
+                                                uint8_t *q, uint32_t *sf, int ld_sf,
+                                                int rows, int K, void *stream);
+
+/*
+ * Gradient of the norm, from its input h as stored (residual_out, or x where
+ * there is no residual); the quantisation is taken as the identity.
+ *   r = 1 / sqrt(mean_k(h^2) + eps),  g = dy * weight
+ *   dx = dres + r * (g - h * r^2 * mean_k(g * h))   [rows][K], h's type
+ *   dw = sum over rows of dy * h * r                [K] fp32
+ *   dy [rows][K]; h, dres (or NULL = 0), dx [rows][K] of one type; dx may be
+ *   dres or h (in place).  dx is the gradient of x and of the residual alike.
+ * dw is added up in a fixed order: the same bits on every run.
+ *   workspace: dg_get_rmsnorm_backward_workspace_size(rows, K) bytes of device
+ *   memory, 16-byte aligned (NULL when that is 0), of any content.
+ * Errors as above, and DG_ERR_ARG for a workspace that is too small.
+ */
+int dg_rmsnorm_backward(const void *dy, int dy_type, const void *h, int h_type,
+                        const void *weight, int weight_type, float eps,
+                        const void *dres, void *dx, float *dw, int rows, int K,
+                        void *workspace, size_t workspace_bytes, void *stream);
+int64_t dg_get_rmsnorm_backward_workspace_size(int rows, int K);
+
+/*
+ * Gated projections: both GEMMs, the activation and the product in one kernel.
+ *   gate = A . Wg^T,  up = A . Wu^T  (block-scaled as in dg_fp8_gemm_nt)
+ *   h = act(gate) * up
+ *   a [M][K], sfa [K/128][ld_sfa]  as for dg_fp8_gemm_nt
+ *   b [2][I][K] E4M3               Wg, then Wu
+ *   sfb [2][ceil(I/128)][K/128]    (what dg_quantize_e4m3_128x128 writes for
+ *                                  two groups of I rows)
+ *   gu [M][2][I] bf16              optional: gate and up, for the backward pass
+ *   h [M][I] bf16                  optional
+ *   q [M][I] E4M3, sf [I/128][ld_sf] fp32   optional: h through the 1x128
+ *                                  quantiser (before any rounding), the A
+ *                                  operand of the next GEMM; needs I % 128 == 0
+ * h or q is needed; act is a dg_act.
+ * The _ue8m0_packed form takes packed power-of-two scales (sfa
+ * [ceil(K/512)][ld_sfa], sfb [2][ceil(I/128)][ceil(K/512)]) and writes such
+ * scales (sf [ceil(I/512)][ld_sf]), as dg_fp8_gemm_nt_ue8m0_packed takes them.
+ *   workspace: as for dg_fp8_gemm_nt_ws (zeroed once by the caller, left with
+ *   its counters zero), dg_get_gated_workspace_size(M, I, K) bytes; NULL, or a
+ *   size of 0, runs without splitting the work of small M any further.
+ * Errors: DG_ERR_NULL; DG_ERR_SHAPE (M < 0; I < 1; K < 128 or K % 128; q with
+ * I % 128; 2*I*K or the bytes of sfa reaching 2^31); DG_ERR_ARG (act; a
+ * workspace that is too small); DG_ERR_ALIGN.
+ */
+int dg_fp8_gated_gemm_nt(const uint8_t *a, const float *sfa, int ld_sfa,
+                         const uint8_t *b, const float *sfb, int act,
+                         uint16_t *gu, uint16_t *h, uint8_t *q, float *sf, int ld_sf,
+                         int M, int I, int K,
+                         void *workspace, size_t workspace_bytes, void *stream);
+int dg_fp8_gated_gemm_nt_ue8m0_packed(const uint8_t *a, const uint32_t *sfa, int ld_sfa,
+                                      const uint8_t *b, const uint32_t *sfb, int act,
+                                      uint16_t *gu, uint16_t *h, uint8_t *q, uint32_t *sf, int ld_sf,
+                                      int M, int I, int K,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+int64_t dg_get_gated_workspace_size(int M, int I, int K);
+
+/*
+ * Its M-grouped forms, with the row layouts of the plain M-grouped GEMMs: b
+ * [G][2][I][K], sfb [G][2][ceil(I/128)][K/128].
+ * Contiguous: a, gu, h, q of M_total rows (a multiple of 128), sfa
+ * [K/128][M_total], sf [I/128][M_total], m_indices [M_total] (16-byte aligned).
+ * Masked: a [G][M_cap][K], sfa [G][K/128][round_up(M_cap,4)], outputs
+ * [G][M_cap][..], sf [G][I/128][round_up(M_cap,4)], masked_m [G] on the device.
+ * Rows that hold no data are not written, in any output, sf included.
+ */
+int dg_m_grouped_fp8_gated_gemm_nt_contiguous(const uint8_t *a, const float *sfa,
+                                              const uint8_t *b, const float *sfb, int act,
+                                              uint16_t *gu, uint16_t *h, uint8_t *q, float *sf,
+                                              const int32_t *m_indices,
+                                              int M_total, int I, int K, int G, void *stream);
+int dg_m_grouped_fp8_gated_gemm_nt_contiguous_ue8m0_packed(const uint8_t *a, const uint32_t *sfa,
+                                                           const uint8_t *b, const uint32_t *sfb, int act,
+                                                           uint16_t *gu, uint16_t *h, uint8_t *q, uint32_t *sf,
+                                                           const int32_t *m_indices,
+                                                           int M_total, int I, int K, int G, void *stream);
+int dg_m_grouped_fp8_gated_gemm_nt_masked(const uint8_t *a, const float *sfa,
+                                          const uint8_t *b, const float *sfb, int act,
+                                          uint16_t *gu, uint16_t *h, uint8_t *q, float *sf,
+                                          const int32_t *masked_m,
+                                          int G, int M_cap, int I, int K, int expected_m, void *stream);
+int dg_m_grouped_fp8_gated_gemm_nt_masked_ue8m0_packed(const uint8_t *a, const uint32_t *sfa,
+                                                       const uint8_t *b, const uint32_t *sfb, int act,
+                                                       uint16_t *gu, uint16_t *h, uint8_t *q, uint32_t *sf,
+                                                       const int32_t *masked_m,
+                                                       int G, int M_cap, int I, int K, int expected_m,
+                                                       void *stream);
+
+/*
+ * Gradient of h = act(gate) * up, quantised for the gradient GEMMs that follow:
+ *   d_gate = dh * up * act'(gate),  d_up = dh * act(gate)
+ *   gu [rows][2][I] bf16 (as saved by the gated GEMM), dh [rows][I] bf16
+ *   m_indices [rows] int32 or NULL: rows with a negative index count as zeros
+ *       in every output (whatever gu and dh hold there), so the padding of the
+ *       contiguous layout adds nothing to a weight gradient
+ * Outputs, each optional, at least one:
+ *   dgu [rows][2][I] bf16                        d_gate, d_up
+ *   q [rows][2I] E4M3, sf [2I/128][ld_sf]        1x128 scales along 2I: the A
+ *       operand of the input gradient, d_x = [d_gate d_up] . [Wg; Wu]
+ *   qt [rows up to a multiple of 128][2I] E4M3, sft [ceil(rows/128)][2I]   one
+ *       scale per column and 128 rows: the A operand, stored [K][M], of
+ *       dg_fp8_gemm_tn and dg_k_grouped_fp8_gemm_tn_contiguous for the weight
+ *       gradient of [Wg; Wu]; rows past the last are written as zeros
+ *   ht [.. as qt ..][I] E4M3, sfht [ceil(rows/128)][I]   the same of h =
+ *       act(gate) * up, for the weight gradient of the projection that follows
+ * The _ue8m0 form rounds every scale up to a power of two.
+ * Errors: DG_ERR_NULL; DG_ERR_SHAPE (rows < 0; I < 128 or I % 128); DG_ERR_ARG
+ * (act); DG_ERR_ALIGN (m_indices: 4 bytes, the others 16; ld_sf < rows or
+ * ld_sf % 4).
+ */
+int dg_gated_backward_quantize_e4m3(const uint16_t *gu, const uint16_t *dh, int act, const int32_t *m_indices,
+                                    uint16_t *dgu, uint8_t *q, float *sf, int ld_sf,
+                                    uint8_t *qt, float *sft, uint8_t *ht, float *sfht,
+                                    int rows, int I, void *stream);
+int dg_gated_backward_quantize_e4m3_ue8m0(const uint16_t *gu, const uint16_t *dh, int act, const int32_t *m_indices,
+                                          uint16_t *dgu, uint8_t *q, float *sf, int ld_sf,
+                                          uint8_t *qt, float *sft, uint8_t *ht, float *sfht,
+                                          int rows, int I, void *stream);
 
 /* Row alignment of expert segments in the contiguous layout (128): the
  * set_/get_mk_alignment_for_contiguous_layout utilities of the "DeepGEMM"

@@ -12,6 +12,12 @@ __all__ = [
     "m_grouped_fp8_gemm_nt_masked",
     "quantize_e4m3_1x128",
     "quantize_e4m3_128x128",
+    "rmsnorm_quantize_e4m3_1x128",
+    "rmsnorm_backward",
+    "fp8_gated_gemm_nt",
+    "m_grouped_fp8_gated_gemm_nt_contiguous",
+    "m_grouped_fp8_gated_gemm_nt_masked",
+    "gated_backward_quantize_e4m3",
     "get_mk_alignment_for_contiguous_layout",
     "set_mk_alignment_for_contiguous_layout",
     "get_sf_aligned_size",

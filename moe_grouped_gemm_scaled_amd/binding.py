@@ -24,6 +24,8 @@ DG_OK = 0
 _STATUS = {0: "DG_OK", -1: "DG_ERR_NULL", -2: "DG_ERR_SHAPE", -3: "DG_ERR_ALIGN", -4: "DG_ERR_ARG",
            -5: "DG_ERR_UNSUPPORTED", -6: "DG_ERR_HIP", -7: "DG_ERR_SCRATCH"}
 
+_P = ct.c_void_p
+
 EXPORTS = {
     # name: (restype, argtypes)
     "dg_fp8_gemm_nt": (ct.c_int, [ct.c_void_p, ct.c_void_p, ct.c_int, ct.c_void_p, ct.c_void_p, ct.c_void_p,
@@ -93,6 +95,25 @@ EXPORTS = {
                                      ct.c_void_p, ct.c_int, ct.c_void_p, ct.c_int, ct.c_int, ct.c_int, ct.c_int,
                                      ct.c_void_p]),
     "dg_get_mk_alignment_for_contiguous_layout": (ct.c_int, []),
+    **{name: (ct.c_int, [_P, ct.c_int, ct.c_int64, _P, ct.c_int, _P, ct.c_int, ct.c_float, _P, _P, _P, _P, ct.c_int,
+                         ct.c_int, ct.c_int, _P])
+       for name in ("dg_rmsnorm_quantize_e4m3_1x128", "dg_rmsnorm_quantize_e4m3_1x128_ue8m0",
+                    "dg_rmsnorm_quantize_e4m3_1x128_ue8m0_packed")},
+    "dg_rmsnorm_backward": (ct.c_int, [_P, ct.c_int, _P, ct.c_int, _P, ct.c_int, ct.c_float, _P, _P, _P, ct.c_int,
+                                       ct.c_int, _P, ct.c_size_t, _P]),
+    "dg_get_rmsnorm_backward_workspace_size": (ct.c_int64, [ct.c_int, ct.c_int]),
+    **{name: (ct.c_int, [_P, _P, ct.c_int, _P, _P, ct.c_int, _P, _P, _P, _P, ct.c_int, ct.c_int, ct.c_int, ct.c_int,
+                         _P, ct.c_size_t, _P])
+       for name in ("dg_fp8_gated_gemm_nt", "dg_fp8_gated_gemm_nt_ue8m0_packed")},
+    "dg_get_gated_workspace_size": (ct.c_int64, [ct.c_int, ct.c_int, ct.c_int]),
+    **{name: (ct.c_int, [_P, _P, _P, _P, ct.c_int, _P, _P, _P, _P, _P, ct.c_int, ct.c_int, ct.c_int, ct.c_int, _P])
+       for name in ("dg_m_grouped_fp8_gated_gemm_nt_contiguous",
+                    "dg_m_grouped_fp8_gated_gemm_nt_contiguous_ue8m0_packed")},
+    **{name: (ct.c_int, [_P, _P, _P, _P, ct.c_int, _P, _P, _P, _P, _P, ct.c_int, ct.c_int, ct.c_int, ct.c_int,
+                         ct.c_int, _P])
+       for name in ("dg_m_grouped_fp8_gated_gemm_nt_masked", "dg_m_grouped_fp8_gated_gemm_nt_masked_ue8m0_packed")},
+    **{name: (ct.c_int, [_P, _P, ct.c_int, _P, _P, _P, _P, ct.c_int, _P, _P, _P, _P, ct.c_int, ct.c_int, _P])
+       for name in ("dg_gated_backward_quantize_e4m3", "dg_gated_backward_quantize_e4m3_ue8m0")},
     "dg_set_mk_alignment_for_contiguous_layout": (ct.c_int, [ct.c_int]),
     "dg_get_sf_aligned_size": (ct.c_int, [ct.c_int]),
     "dg_set_num_cus": (ct.c_int, [ct.c_int]),
@@ -412,6 +433,272 @@ def fp8_mqa_logits(q, kv, kv_scale, weights, k_start, k_end, clean_logits=True, 
             _ptr(logits, torch.float32, "logits", (S, S_kv)), S, H, D, S_kv, _stream(q))
     _check(lib().dg_fp8_mqa_logits(*args), "dg_fp8_mqa_logits")
     return logits
+
+
+# ---------------------------------------------------------------- the feed-forward layer
+
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+_ACTS = {"silu": 0, "gelu": 1}
+_SUFFIX = {"fp32": "", "ue8m0": "_ue8m0", "ue8m0_packed": "_ue8m0_packed"}
+
+
+def _raw(t, dtype, shape, name):
+    """The address of a dense device tensor of this type (one of a tuple, or any when None) and shape; None for None."""
+    if t is None:
+        return None
+    if dtype is not None and t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _type_of(t, name):
+    try:
+        return _TYPES[t.dtype]
+    except KeyError:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float32") from None
+
+
+def _act_of(act):
+    try:
+        return _ACTS[act]
+    except KeyError:
+        raise ValueError(f"act {act!r}, expected one of {tuple(_ACTS)}") from None
+
+
+def _out(t, shape, dtype, device, zero=False):
+    """An output argument: a tensor as given, a new one for True, None otherwise."""
+    if t is True:
+        return torch.zeros(shape, dtype=dtype, device=device) if zero else torch.empty(shape, dtype=dtype, device=device)
+    return None if t is False else t
+
+
+def _call(name, *args):
+    status = getattr(lib(), name)(*args)
+    if status != DG_OK:
+        raise DGError(status, name)
+
+
+def _queue(t):
+    """The current stream of a tensor's device, which has to be the current device (kernels run there)."""
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensors on device {t.get_device()}, but the current device is {torch.cuda.current_device()}")
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _sf_rows(scales, kblocks):
+    return (kblocks + 3) // 4 if scales == "ue8m0_packed" else kblocks
+
+
+def rmsnorm_quantize_e4m3_1x128(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, q=None, sf=None,
+                                ld_sf=None, scales="fp32"):
+    """h = x + residual, RMS norm of h times weight, 1x128 E4M3 quantisation, in one pass
+    (dg_rmsnorm_quantize_e4m3_1x128[_ue8m0[_packed]]).
+
+    x[rows, K] bf16 or fp32 (rows may be strided, columns dense), weight[K] bf16 or fp32; residual[rows, K] bf16 or
+    fp32, with residual_out (allocated when None; may be the residual itself) receiving h; y: a bf16 [rows, K] tensor
+    to fill, or True for a new one; scales "fp32" or "ue8m0" (sf[K/128, ld_sf] fp32) or "ue8m0_packed"
+    (sf[ceil(K/512), ld_sf] int32).  q=False leaves the quantised output out (y is needed then).
+    Returns (q, sf, residual_out, y), None where not asked for."""
+    if scales not in _SUFFIX:
+        raise ValueError(f"scales {scales!r}, expected one of {tuple(_SUFFIX)}")
+    if x.dim() != 2 or not x.is_cuda or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x: a device tensor [rows, K] with dense columns")
+    rows, K = x.shape
+    shape = x.shape
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+    elif residual_out is None:
+        residual_out = torch.empty_like(residual)
+    y = _out(y, shape, torch.bfloat16, x.device)
+    sf_t = torch.int32 if scales == "ue8m0_packed" else torch.float32
+    if q is False:
+        q = sf = None
+        ld = 0
+    else:
+        ld = (sf.shape[-1] if sf is not None else (rows + 3) // 4 * 4) if ld_sf is None else int(ld_sf)
+        n = _sf_rows(scales, K // 128)
+        if q is None:
+            q = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        if sf is None:
+            sf = torch.zeros((n, ld), dtype=sf_t, device=x.device)
+    _call("dg_rmsnorm_quantize_e4m3_1x128" + _SUFFIX[scales], x.data_ptr(), _type_of(x, "x"),
+          x.stride(0) if rows > 1 else K,
+          _raw(residual, None, shape, "residual"), 0 if residual is None else _type_of(residual, "residual"),
+          _raw(weight, None, (K,), "weight"), _type_of(weight, "weight"), eps,
+          _raw(residual_out, None if residual is None else residual.dtype, shape, "residual_out"),
+          _raw(y, torch.bfloat16, shape, "y"), _raw(q, _FP8, shape, "q"),
+          None if q is None else _raw(sf, sf_t, (n, ld), "sf"), ld, rows, K, _queue(x))
+    return q, sf, residual_out, y
+
+
+def get_rmsnorm_backward_workspace_size(rows: int, K: int) -> int:
+    """Bytes of scratch rmsnorm_backward needs on the current device (of any content)."""
+    v = lib().dg_get_rmsnorm_backward_workspace_size(int(rows), int(K))
+    if v < 0:
+        raise DGError(int(v), "dg_get_rmsnorm_backward_workspace_size")
+    return int(v)
+
+
+def rmsnorm_backward(dy, h, weight, eps=1e-6, dres=None, dx=None, dw=None, workspace="auto"):
+    """Gradient of the RMS norm (dg_rmsnorm_backward): dy[rows, K] bf16 or fp32, h[rows, K] the norm's input as stored
+    (bf16 or fp32), dres[rows, K] of h's type the gradient arriving at h itself (or None); returns (dx of h's type,
+    dw[K] fp32).  dx may be dres or h.  workspace: a uint8 device tensor of get_rmsnorm_backward_workspace_size bytes,
+    or "auto"."""
+    shape = h.shape
+    if len(shape) != 2:
+        raise ValueError(f"h: shape {tuple(shape)}, expected [rows, K]")
+    rows, K = shape
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError(f"workspace {workspace!r}")
+        n = get_rmsnorm_backward_workspace_size(rows, K)
+        workspace = torch.empty(n, dtype=torch.uint8, device=h.device) if n else None
+    if dx is None:
+        dx = torch.empty_like(h)
+    if dw is None:
+        dw = torch.empty(K, dtype=torch.float32, device=h.device)
+    _call("dg_rmsnorm_backward", _raw(dy, None, shape, "dy"), _type_of(dy, "dy"), _raw(h, None, shape, "h"),
+          _type_of(h, "h"), _raw(weight, None, (K,), "weight"), _type_of(weight, "weight"), eps,
+          _raw(dres, h.dtype, shape, "dres"), _raw(dx, h.dtype, shape, "dx"), _raw(dw, torch.float32, (K,), "dw"),
+          rows, K, None if workspace is None else _raw(workspace, torch.uint8, workspace.shape, "workspace"),
+          0 if workspace is None else workspace.numel(), _queue(h))
+    return dx, dw
+
+
+def get_gated_workspace_size(M: int, I: int, K: int) -> int:
+    """Bytes of scratch fp8_gated_gemm_nt can use on the current device (0: none)."""
+    v = lib().dg_get_gated_workspace_size(int(M), int(I), int(K))
+    if v < 0:
+        raise DGError(int(v), "dg_get_gated_workspace_size")
+    return int(v)
+
+
+def get_gated_workspace(M: int, I: int, K: int, device=None):
+    """A zero-filled uint8 device tensor of get_gated_workspace_size(M, I, K) bytes (None when that is 0).  It may
+    serve any number of fp8_gated_gemm_nt calls in stream order; calls that can run at the same time each need
+    their own."""
+    n = get_gated_workspace_size(M, I, K)
+    return torch.zeros(n, dtype=torch.uint8, device=device if device is not None else "cuda") if n else None
+
+
+def _gated_args(a, sfa, b, sfb, act, h, q, sf, gu, lead, G, rows, ld):
+    """Arguments that the three layouts of the gated GEMM share, and the outputs: lead = leading dimensions of the
+    row tensors, G = leading dimensions of b."""
+    I, K = b.shape[-2], b.shape[-1]
+    packed = sfa.dtype is torch.int32
+    scales = "ue8m0_packed" if packed else "fp32"
+    sf_t = torch.int32 if packed else torch.float32
+    n, blocks = _sf_rows(scales, K // 128), (I + 127) // 128
+    if h is None and q is None and sf is None:
+        h = True
+    partial = len(G) > 0                       # rows without data keep what the buffers hold
+    dev = a.device
+    h = _out(h, (*lead, rows, I), torch.bfloat16, dev, partial)
+    gu = _out(gu, (*lead, rows, 2 * I), torch.bfloat16, dev, partial)
+    q = _out(q, (*lead, rows, I), torch.uint8, dev, partial)
+    shape_sf = (*lead, _sf_rows(scales, blocks), ld)
+    if q is not None and (sf is None or sf is True):
+        sf = torch.zeros(shape_sf, dtype=sf_t, device=dev)
+    if gu is not None and gu.dim() == len(lead) + 3:
+        gu_shape = (*lead, rows, 2, I)
+    else:
+        gu_shape = (*lead, rows, 2 * I)
+    ins = (_raw(a, _FP8, (*lead, rows, K), "a"), _raw(sfa, sf_t, (*lead, n, ld), "sfa"),
+           _raw(b, _FP8, (*G, 2, I, K), "b"), _raw(sfb, sf_t, (*G, 2, blocks, n), "sfb"))
+    outs = (_raw(gu, torch.bfloat16, gu_shape, "gu"), _raw(h, torch.bfloat16, (*lead, rows, I), "h"),
+            _raw(q, _FP8, (*lead, rows, I), "q"), None if q is None else _raw(sf, sf_t, shape_sf, "sf"))
+    return ins, _act_of(act), outs, (h, q, sf if q is not None else None, gu), I, K, _SUFFIX[scales]
+
+
+def fp8_gated_gemm_nt(a, sfa, b, sfb, act="silu", h=None, q=None, sf=None, gu=None, workspace="auto"):
+    """h = act(A Wg^T) * (A Wu^T) in one kernel (dg_fp8_gated_gemm_nt): a[M, K], sfa[K/128, ld], b[2, I, K] (Wg, Wu),
+    sfb[2, ceil(I/128), K/128]; int32 sfa and sfb are packed power-of-two scales (dg_fp8_gated_gemm_nt_ue8m0_packed).
+    act "silu" or "gelu" (tanh form).  Outputs: a tensor to fill, or True for a new one: h[M, I] bf16 (the default),
+    q[M, I] E4M3 with sf[I/128 (packed: ceil(I/512)), ld], gu[M, 2I] bf16 (gate, up).  workspace as for fp8_gemm_nt,
+    from get_gated_workspace().  Returns (h, q, sf, gu), None where not asked for."""
+    if a.dim() != 2 or b.dim() != 3 or sfa.dim() != 2:
+        raise ValueError("a[M, K], sfa[K/128, ld], b[2, I, K]")
+    M = a.shape[0]
+    ld = sfa.shape[1]
+    ins, act_id, outs, ret, I, K, suffix = _gated_args(a, sfa, b, sfb, act, h, q, sf, gu, (), (), M, ld)
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError(f"workspace {workspace!r}")
+        workspace = get_gated_workspace(M, I, K, a.device)
+    _call("dg_fp8_gated_gemm_nt" + suffix, ins[0], ins[1], ld, ins[2], ins[3], act_id, *outs, ld, M, I, K,
+          None if workspace is None else _raw(workspace, torch.uint8, workspace.shape, "workspace"),
+          0 if workspace is None else workspace.numel(), _queue(a))
+    return ret
+
+
+def m_grouped_fp8_gated_gemm_nt_contiguous(a, sfa, b, sfb, m_indices, act="silu", h=None, q=None, sf=None, gu=None):
+    """The gated GEMM in the contiguous layout: a[M_total, K], sfa[K/128, M_total], b[G, 2, I, K],
+    sfb[G, 2, ceil(I/128), K/128], m_indices[M_total] int32; outputs as fp8_gated_gemm_nt (ld = M_total), new ones
+    zero on the rows without data."""
+    if a.dim() != 2 or b.dim() != 4:
+        raise ValueError("a[M_total, K], b[G, 2, I, K]")
+    M, G = a.shape[0], b.shape[0]
+    ins, act_id, outs, ret, I, K, suffix = _gated_args(a, sfa, b, sfb, act, h, q, sf, gu, (), (G,), M, M)
+    _call("dg_m_grouped_fp8_gated_gemm_nt_contiguous" + suffix, *ins, act_id, *outs,
+          _raw(m_indices, torch.int32, (M,), "m_indices"), M, I, K, G, _queue(a))
+    return ret
+
+
+def m_grouped_fp8_gated_gemm_nt_masked(a, sfa, b, sfb, masked_m, expected_m=0, act="silu", h=None, q=None, sf=None,
+                                       gu=None):
+    """The gated GEMM in the masked layout: a[G, M_cap, K], sfa[G, K/128, round_up(M_cap, 4)], b[G, 2, I, K],
+    sfb[G, 2, ceil(I/128), K/128], masked_m[G] int32; outputs with a leading G, new ones zero on the rows without
+    data."""
+    if a.dim() != 3 or b.dim() != 4:
+        raise ValueError("a[G, M_cap, K], b[G, 2, I, K]")
+    G, M = a.shape[0], a.shape[1]
+    ld = (M + 3) // 4 * 4
+    ins, act_id, outs, ret, I, K, suffix = _gated_args(a, sfa, b, sfb, act, h, q, sf, gu, (G,), (G,), M, ld)
+    _call("dg_m_grouped_fp8_gated_gemm_nt_masked" + suffix, *ins, act_id, *outs,
+          _raw(masked_m, torch.int32, (G,), "masked_m"), G, M, I, K, int(expected_m), _queue(a))
+    return ret
+
+
+def gated_backward_quantize_e4m3(gu, dh, act="silu", m_indices=None, dgu=None, q=None, sf=None, qt=None, sft=None,
+                                 ht=None, sfht=None, ue8m0=False):
+    """Gradient of h = act(gate) * up, quantised (dg_gated_backward_quantize_e4m3[_ue8m0]): gu[rows, 2I] and
+    dh[rows, I] bf16, m_indices[rows] int32 or None (rows with a negative index count as zeros).  Outputs, each a tensor to fill or
+    True for a new one (scales are allocated with their codes): dgu[rows, 2I] bf16; q[rows, 2I] with sf[2I/128, ld];
+    qt[R, 2I] with sft[R/128, 2I] and ht[R, I] with sfht[R/128, I], R = rows up to a multiple of 128.
+    Returns (dgu, q, sf, qt, sft, ht, sfht), None where not asked for."""
+    if dh.dim() != 2:
+        raise ValueError("dh[rows, I]")
+    rows, I = dh.shape
+    full = (rows + 127) // 128
+    dev = dh.device
+    f32 = torch.float32
+    dgu = _out(dgu, (rows, 2 * I), torch.bfloat16, dev)
+    q, qt, ht = (_out(q, (rows, 2 * I), torch.uint8, dev), _out(qt, (full * 128, 2 * I), torch.uint8, dev),
+                 _out(ht, (full * 128, I), torch.uint8, dev))
+    if q is not None and sf is None:
+        sf = torch.zeros((2 * I // 128, (rows + 3) // 4 * 4), dtype=f32, device=dev)
+    if qt is not None and sft is None:
+        sft = torch.empty((full, 2 * I), dtype=f32, device=dev)
+    if ht is not None and sfht is None:
+        sfht = torch.empty((full, I), dtype=f32, device=dev)
+    ld = sf.shape[-1] if q is not None else 0
+    bf16 = torch.bfloat16
+    _call("dg_gated_backward_quantize_e4m3" + ("_ue8m0" if ue8m0 else ""),
+          _raw(gu, bf16, (rows, 2, I) if gu.dim() == 3 else (rows, 2 * I), "gu"), _raw(dh, bf16, (rows, I), "dh"),
+          _act_of(act), _raw(m_indices, torch.int32, (rows,), "m_indices"), _raw(dgu, bf16, (rows, 2 * I), "dgu"),
+          _raw(q, _FP8, (rows, 2 * I), "q"), None if q is None else _raw(sf, f32, (2 * I // 128, ld), "sf"), ld,
+          _raw(qt, _FP8, (full * 128, 2 * I), "qt"), None if qt is None else _raw(sft, f32, (full, 2 * I), "sft"),
+          _raw(ht, _FP8, (full * 128, I), "ht"), None if ht is None else _raw(sfht, f32, (full, I), "sfht"),
+          rows, I, _queue(dh))
+    return (dgu, q, sf if q is not None else None, qt, sft if qt is not None else None, ht,
+            sfht if ht is not None else None)
 
 
 def get_mk_alignment_for_contiguous_layout() -> int:

@@ -13,6 +13,7 @@
 
 #include "../../include/dg.h"
 #include "dg_internal.h"
+#include "dg_layer.h"
 
 namespace {
 
@@ -99,6 +100,16 @@ int kernel_family_from_name(const char *name) {
 }
 
 const char *kernel_family_name(int f) { return f >= 0 && f < kFamilies ? kFamilyNames[f] : "auto"; }
+
+int current_device_cus(int &cus) {
+    int dev = 0;
+    return current_device(dev, cus);
+}
+
+void set_last_config(const std::string &config) {
+    t_last_config = config;
+    if (print_configs()) fprintf(stderr, "[dg] %s\n", config.c_str());
+}
 
 static int family_from_env() {
     static const int v = [] {

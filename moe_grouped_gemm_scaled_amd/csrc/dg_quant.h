@@ -1,0 +1,52 @@
+// dg_quant.h -- E4M3 quantisation of one block, shared by the kernels that
+// write quantised tensors: the block scale sf = max(amax, 1e-4) / 448 (fp32,
+// or rounded up to a power of two) and the codes of x / sf.
+#pragma once
+
+#include "dg_device.h"
+
+namespace dg {
+
+// Four quotients x / s, already rounded to fp32, to E4M3FN codes (byte i
+// from element i) with gfx950's packed conversion.  For every finite |v| <
+// 464 it gives the nearest E4M3FN value, ties to the even code, subnormals
+// (steps of 2^-9 below 2^-6) included, which was checked against a software
+// encoder over all 2^32 fp32 inputs.  Above 464 it does not saturate, but a
+// block's values divided by its scale stay below 448 * (1 + 2^-23).  NaN keeps
+// its sign through the conversion; NaN codes are made positive (0x7f) here,
+// the quantisers' NaN code.
+__device__ __forceinline__ uint32_t e4m3_encode4(float a, float b, float c, float d) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+    const uint32_t u = (uint32_t)w;
+    const uint32_t nan = ((u & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // bytes whose low 7 bits are all ones
+    return u & ~nan;
+}
+
+// x / s rounded to fp32 (IEEE division), for finite s > 0, from y = 1/s
+// rounded to fp64: RN32(x * y) with the product rounded to fp64 first.  This
+// is exact: a quotient of two fp32 values is never closer than 2^-49
+// (relative) to a point halfway between two fp32 values, while the two fp64
+// roundings move it by less than 2^-51, so both round to the same fp32.
+// (x = +-inf or NaN gives NaN, as the division does; s = inf gives y = 0.)
+__device__ __forceinline__ float div_by_scale(float x, double y) { return (float)((double)x * y); }
+
+// The block's four quotients as codes.  Power-of-two scales: multiplying by
+// the exact reciprocal is the division.
+template <bool UE8M0>
+__device__ __forceinline__ uint32_t encode_block4(const v4f &v, float inv, double y) {
+    if constexpr (UE8M0) return e4m3_encode4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    return e4m3_encode4(div_by_scale(v.x, y), div_by_scale(v.y, y), div_by_scale(v.z, y), div_by_scale(v.w, y));
+}
+
+template <bool UE8M0>
+__device__ __forceinline__ float block_scale(float amax) {
+    const float s = fmaxf(amax, 1e-4f) / 448.0f;          // IEEE division (no fast-math)
+    if constexpr (!UE8M0) return s;
+    // s is a normal fp32 (>= 1e-4/448): clear the mantissa and, if it was not
+    // zero, step the exponent up by one
+    const uint32_t u = __float_as_uint(s);
+    return __uint_as_float((u & 0x7fffffu) ? (u & 0x7f800000u) + 0x00800000u : u);
+}
+
+}  // namespace dg

@@ -1,0 +1,463 @@
+// gated.hip -- the first half of a gated feed-forward block on gfx950 in one
+// kernel: both FP8 block-scaled projections, the activation and the product,
+// with a bf16 or an E4M3 output.
+//
+//     gate = A . Wg^T,  up = A . Wu^T   (b holds Wg, then Wu: [2][I][K])
+//     h = act(gate) * up
+//
+// Arithmetic of the projections as in the plain GEMM: one
+// v_mfma_f32_16x16x128_f8f6f4 partial per 16x16 subtile and 128-wide K block,
+// promoted into fp32 with sfa * sfb (packed power-of-two scales: applied by
+// the scaled MFMA itself).  Nothing is rounded before the outputs.
+//
+// Organisation: the LDS-DMA pipeline of the plain GEMM (constant-count waits,
+// XOR-swizzled stages, see pipelined.hip), with a column tile that holds the
+// same 128 columns of both projections: of the 64 B rows that a wave
+// multiplies, 32 are gate rows and 32 the up rows of the same columns, so a
+// lane ends up with both factors of its h values in its own registers and the
+// product needs no exchange.  128 columns are also one quantisation block of
+// the next GEMM's K axis: a row's scale is a maximum over the tile's row,
+// four values per row through LDS.  Outputs are staged in LDS as whole rows,
+// so that every store instruction writes whole lines.
+#include <stdio.h>
+
+#include "dg_act.h"
+#include "dg_internal.h"
+#include "dg_layer.h"
+#include "dg_pipeline.h"
+#include "dg_quant.h"
+
+namespace dg {
+
+struct GatedArgs {
+    const uint8_t *a;
+    const float *sfa;
+    const uint8_t *b;
+    const float *sfb;
+    const int32_t *idx;        // m_indices (contiguous) or masked_m (masked)
+    uint16_t *gu, *h;
+    uint8_t *q;
+    void *sf;
+    int rows_a, I, K, ld_sfa, ld_sf, G, act;
+    int tiles_m, tiles_n, gm;
+};
+
+// 16-byte chunk c of row r in a staged output tile of CPR chunks per row: the
+// chunk index is XORed with the row, so that the 16 rows that a wave writes
+// together fall on different banks.
+template <int CPR>
+__device__ __forceinline__ int staged(int r, int c) {
+    return (r * CPR + (c ^ (r & (CPR - 1)))) * 16;
+}
+
+template <int BM, int WGM, int WGN, int NST, Mode MODE, bool PK>
+__global__ void __launch_bounds__(64 * WGM * WGN)
+gated_kernel(GatedArgs p) {
+    constexpr int BN = 256, BH = 128;             // B rows of a tile, columns of h
+    constexpr int NW = WGM * WGN;
+    constexpr int TM = BM / WGM, TN = BN / WGN;   // wave tile
+    constexpr int TH = TN / 2;                    // columns of h per wave
+    constexpr int SM = TM / 16, SN = TN / 16;     // MFMA subtiles per wave
+    constexpr int SH = SN / 2;                    // of them gate (the others up)
+    constexpr int BLK_A = BM * kKBlock, BLK_B = BN * kKBlock;
+    constexpr int OFF_B = BLK_A;
+    constexpr int OFF_SA = OFF_B + BLK_B;         // sfa[kb][m0 + 4l .. +3] at 16 l
+    constexpr int OFF_SB = OFF_SA + 1024;         // gate, up: 16 bytes of sfb from K block kb
+    constexpr int OFF_JUNK = OFF_SB + 1024;       // scale loads of the waves that fetch none (zeros)
+    constexpr int STAGE = OFF_JUNK + 1024;
+    constexpr int DA = BM / (8 * NW), DB = BN / (8 * NW);   // 1-KB LDS-DMA chunks per wave per K block
+    constexpr int PER_BLOCK = DA + DB + 1;
+    static_assert(NST >= 2 && NST <= 3 && NST * STAGE + BM * WGN * 4 <= 160 * 1024, "LDS");
+    static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM / 4 <= 64 && NW >= 2, "DMA chunks");
+    static_assert((NST - 2) * PER_BLOCK < 64, "vmcnt immediate");
+    static_assert(TH % 16 == 0 && BM * 256 <= STAGE, "a staged output tile fits one stage");
+
+    __shared__ __attribute__((aligned(16))) uint8_t stage0[STAGE];
+    __shared__ __attribute__((aligned(16))) uint8_t stage1[STAGE];
+    __shared__ __attribute__((aligned(16))) uint8_t stage2[NST > 2 ? STAGE : 16];
+    __shared__ float row_max[WGN][BM];
+    auto stage_of = [&](auto sc) __attribute__((always_inline)) -> uint8_t * {
+        constexpr int s = decltype(sc)::value;
+        if constexpr (s == 0) return stage0;
+        else if constexpr (s == 1) return stage1;
+        else return stage2;
+    };
+
+    const int K = p.K, I = p.I;
+    const int nkb = K / kKBlock;
+    const int nnb = (I + 127) / 128;
+    const int nkw = PK ? (nkb + 3) / 4 : nkb;
+    const int tiles_per_group = p.tiles_m * p.tiles_n;
+    int t_lin = xcd_remap(blockIdx.x, gridDim.x);
+    int grp = 0;
+    if (MODE == Mode::Masked) {
+        grp = t_lin / tiles_per_group;
+        t_lin -= grp * tiles_per_group;
+    }
+    int tm, tn;
+    raster(t_lin, p.tiles_m, p.tiles_n, p.gm, tm, tn);
+    int m0 = tm * BM;
+    if constexpr (MODE == Mode::Contig && BM == 256) {
+        const int ub = __builtin_amdgcn_readfirstlane(contig_unit_block(p.idx, p.rows_a / 128, tm));
+        if (ub < 0) return;                        // no such unit: uniform exit
+        m0 = ub * 128;
+    }
+    const int n0 = tn * BH;
+
+    const uint8_t *A = p.a;
+    const float *SFA = p.sfa;
+    const uint8_t *B = p.b;
+    const float *SFB = p.sfb;
+    int64_t row_base = 0;                          // output row of row 0
+    const int ld = p.ld_sfa;
+    int rows = p.rows_a - m0;                      // rows of the tile that hold data
+    int expert = 0;
+    int64_t sf_base = 0;                           // of the group's output scales
+    if (MODE == Mode::Masked) {
+        const int mm = min(max(p.idx[grp], 0), p.rows_a);
+        if (m0 >= mm) return;                      // uniform exit, before any barrier
+        rows = mm - m0;
+        A += (int64_t)grp * p.rows_a * K;
+        SFA += (int64_t)grp * nkw * ld;
+        B += (int64_t)grp * 2 * I * K;
+        SFB += (int64_t)grp * 2 * nnb * nkw;
+        row_base = (int64_t)grp * p.rows_a;
+        sf_base = (int64_t)grp * (PK ? (nnb + 3) / 4 : nnb) * p.ld_sf;
+    }
+    if (MODE == Mode::Contig) {
+        expert = p.idx[m0];
+        if (expert < 0 || expert >= p.G) return;   // padding (or an invalid id): uniform exit
+        B += (int64_t)expert * 2 * I * K;
+        SFB += (int64_t)expert * 2 * nnb * nkw;
+        if (BM == 256 && !(m0 + 128 < p.rows_a && p.idx[m0 + 128] == expert)) rows = 128;
+    }
+    rows = min(rows, BM);
+    A += (int64_t)m0 * K;
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WGN, wn = wave % WGN;
+    const int l16 = lane & 15;
+    const int g4 = lane >> 4;
+    const bool wave_live = wm * TM < rows;         // the wave has rows to multiply
+
+    // ---- DMA plan: chunk c = wave + NW*i holds tile rows 8c .. 8c+7; lane l
+    // lands at row +l/8, 16-byte chunk l%8 and fetches chunk (l%8) ^ (l/8).
+    // A ends at its last row with data: rows past it read as zeros, with no
+    // memory traffic.  B row r of the tile belongs to wave column r / TN; its
+    // first TH rows are gate rows, the others the up rows of the same columns
+    // (columns past I repeat the last one, and are never stored).
+    const __amdgpu_buffer_rsrc_t rA = __builtin_amdgcn_make_buffer_rsrc((void *)A, (short)0, rows * K, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rB = __builtin_amdgcn_make_buffer_rsrc((void *)B, (short)0, 2 * I * K, 0x00020000);
+    const int dchunk = ((lane & 7) ^ (lane >> 3)) * 16;
+    int va[DA], vb[DB];
+    static_for<DA>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+        va[i] = (8 * (wave + NW * i) + (lane >> 3)) * K + dchunk;
+    });
+    static_for<DB>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+        const int r = 8 * (wave + NW * i) + (lane >> 3);
+        const int o = r % TN;
+        const int col = min(n0 + (r / TN) * TH + o % TH, I - 1);
+        vb[i] = ((o / TH) * I + col) * K + dchunk;
+    });
+    const int lds_a = wave * 1024, lds_b = OFF_B + wave * 1024;
+    // scales: lane l of wave 0 fetches sfa[kb][m0 + 4l .. +3], lanes 0 and 1 of
+    // wave 1 the 16 bytes from K block kb of the gate's and of the up
+    // projection's scale row; every other load points out of range, so that
+    // every wave issues the same number
+    const bool wsa = wave == 0;
+    const __amdgpu_buffer_rsrc_t rS = __builtin_amdgcn_make_buffer_rsrc(
+        wsa ? (void *)SFA : (void *)SFB, (short)0, wsa ? nkw * ld * 4 : 2 * nnb * nkw * 4, 0x00020000);
+    const int sa_row = m0 + 4 * lane;
+    const int v_s = wsa ? (4 * lane < BM && sa_row < ld ? sa_row * 4 : kOutOfRange)
+                        : (wave == 1 && lane < 2 ? (lane * nnb + n0 / 128) * nkw * 4 : kOutOfRange);
+    const int lds_s = wsa ? OFF_SA : (wave == 1 ? OFF_SB : OFF_JUNK);
+    auto dma = [&](uint8_t *stg, int kb) __attribute__((always_inline)) {
+        const int ks = PK ? kb >> 2 : kb;
+        dma_step<DA, DB, NW * 1024, NW * 1024>(stg, rA, rB, rS, va, vb, v_s, lds_a, lds_b, lds_s, kb * kKBlock,
+                                               kb * kKBlock, wsa ? ks * ld * 4 : ks * 4);
+    };
+
+    v4f acc[SM][SN];
+    static_for<SM>([&](auto ic) __attribute__((always_inline)) {
+        static_for<SN>([&](auto jc) __attribute__((always_inline)) {
+            acc[decltype(ic)::value][decltype(jc)::value] = v4f{0.f, 0.f, 0.f, 0.f};
+        });
+    });
+    int off_a0[2], off_b0[2], off_sa;
+    {
+        const int rowa = wm * TM + l16, rowb = wn * TN + l16;
+        off_a0[0] = opaque_offset(rowa * kKBlock + ((g4 ^ (l16 & 7)) << 4));
+        off_a0[1] = opaque_offset(rowa * kKBlock + (((g4 + 4) ^ (l16 & 7)) << 4));
+        off_b0[0] = opaque_offset(OFF_B + rowb * kKBlock + ((g4 ^ (l16 & 7)) << 4));
+        off_b0[1] = opaque_offset(OFF_B + rowb * kKBlock + (((g4 + 4) ^ (l16 & 7)) << 4));
+        off_sa = opaque_offset(OFF_SA + rowa * 4);
+    }
+    auto frag = [&](const uint8_t *lo_p, const uint8_t *hi_p) __attribute__((always_inline)) {
+        const v4i lo = *reinterpret_cast<const v4i *>(lo_p);
+        const v4i hi = *reinterpret_cast<const v4i *>(hi_p);
+        return v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    };
+
+    // Multiply the K block held in `stg`.  The B fragment is the MFMA's first
+    // operand: lane l holds row 16i + l%16 and columns 4(l/16) .. +3 of
+    // subtile (i, j); subtiles j < SH are gate, j + SH the up projection of the
+    // same columns.
+    auto compute = [&](const uint8_t *stg, int kb) __attribute__((always_inline)) {
+        v8i bf[SN];
+        static_for<SN>([&](auto jc) __attribute__((always_inline)) {
+            constexpr int j = decltype(jc)::value;
+            bf[j] = frag(stg + off_b0[0] + j * 16 * kKBlock, stg + off_b0[1] + j * 16 * kKBlock);
+        });
+        if constexpr (PK) {
+            int eb[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                eb[x] = (int)((reinterpret_cast<const uint32_t *>(stg + OFF_SB + 16 * x)[0] >> (8 * (kb & 3))) & 0xffu);
+            static_for<SM>([&](auto ic) __attribute__((always_inline)) {
+                constexpr int i = decltype(ic)::value;
+                const v8i af = frag(stg + off_a0[0] + i * 16 * kKBlock, stg + off_a0[1] + i * 16 * kKBlock);
+                const uint32_t wa = *reinterpret_cast<const uint32_t *>(stg + off_sa + i * 64);
+                const int ea = (int)((wa >> (8 * (kb & 3))) & 0xffu);
+                static_for<SN>([&](auto jc) __attribute__((always_inline)) {
+                    constexpr int j = decltype(jc)::value;
+                    acc[i][j] = mfma_16x16x128_e4m3_scaled(bf[j], af, acc[i][j], eb[j / SH], ea);
+                });
+            });
+        } else {
+            const float sbg = *reinterpret_cast<const float *>(stg + OFF_SB);
+            const float sbu = *reinterpret_cast<const float *>(stg + OFF_SB + 16);
+            auto read_a = [&](auto ic, v8i &af, float &sa) __attribute__((always_inline)) {
+                constexpr int i = decltype(ic)::value;
+                af = frag(stg + off_a0[0] + i * 16 * kKBlock, stg + off_a0[1] + i * 16 * kKBlock);
+                sa = *reinterpret_cast<const float *>(stg + off_sa + i * 64);
+            };
+            // the A fragment of subtile i+1 is read, and subtile i-1 promoted,
+            // while the MFMAs of subtile i run
+            v8i af_cur, af_nxt;
+            float sa_cur, sa_nxt, sa_prv;
+            v4f pp_prv[SN];
+            read_a(std::integral_constant<int, 0>{}, af_cur, sa_cur);
+            static_for<SM>([&](auto ic) __attribute__((always_inline)) {
+                constexpr int i = decltype(ic)::value;
+                if constexpr (i + 1 < SM) read_a(std::integral_constant<int, i + 1>{}, af_nxt, sa_nxt);
+                v4f pp[SN];
+                static_for<SN>([&](auto jc) __attribute__((always_inline)) {
+                    constexpr int j = decltype(jc)::value;
+                    pp[j] = mfma_16x16x128_e4m3(bf[j], af_cur, v4f{0.f, 0.f, 0.f, 0.f});
+                });
+                if constexpr (i > 0) {
+                    static_for<SN>([&](auto jc) __attribute__((always_inline)) {
+                        constexpr int j = decltype(jc)::value;
+                        acc[i - 1][j] = promote(acc[i - 1][j], pp_prv[j], sa_prv * (j < SH ? sbg : sbu));
+                    });
+                }
+                static_for<SN>([&](auto jc) __attribute__((always_inline)) {
+                    pp_prv[decltype(jc)::value] = pp[decltype(jc)::value];
+                });
+                sa_prv = sa_cur;
+                if constexpr (i + 1 < SM) {
+                    af_cur = af_nxt;
+                    sa_cur = sa_nxt;
+                }
+            });
+            static_for<SN>([&](auto jc) __attribute__((always_inline)) {
+                constexpr int j = decltype(jc)::value;
+                acc[SM - 1][j] = promote(acc[SM - 1][j], pp_prv[j], sa_prv * (j < SH ? sbg : sbu));
+            });
+        }
+    };
+
+    // ---- K loop: step j waits for its block, meets the other waves, refills
+    // the stage read in step j-1 and multiplies; it starts NST-1 steps early so
+    // that one copy of every DMA keeps the wait counts exact
+    constexpr int kWaitPipe = wait_vmcnt((NST - 2) * PER_BLOCK);
+#pragma clang loop unroll(disable)
+    for (int b = -(NST - 1); b < nkb; b += NST) {
+        nested_steps<0, NST>(b, nkb, [&](auto sc) __attribute__((always_inline)) {
+            constexpr int u = decltype(sc)::value;
+            const int j = b + u;
+            __builtin_amdgcn_s_waitcnt(kWaitPipe);
+            lds_barrier();
+            dma(stage_of(sc), min(j + NST - 1, nkb - 1));
+            if (j >= 0 && wave_live) compute(stage_of(std::integral_constant<int, (u + 1) % NST>{}), j);
+        });
+    }
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));
+    lds_barrier();
+
+    // ---- epilogue.  Row r of the tile is stored when it holds data (its
+    // output row is row_base + m0 + r).
+    auto row_ok = [&](int r) __attribute__((always_inline)) {
+        bool ok = r < rows;
+        if (MODE == Mode::Contig) ok = ok && p.idx[m0 + r] == expert;
+        return ok;
+    };
+    const int64_t row0 = row_base + m0;
+    // staged bf16 tile (256-byte rows) to columns n0 .. n0+127 of out [..][pitch]
+    auto store_bf16 = [&](const uint8_t *stg, uint16_t *out, int64_t pitch) __attribute__((always_inline)) {
+        const bool vec = (I % 8) == 0;
+        for (int item = tid; item < BM * 16; item += 64 * NW) {
+            const int r = item >> 4, c = item & 15;
+            const int col = n0 + 8 * c;
+            if (!row_ok(r) || col >= I) continue;
+            const v4i v = *reinterpret_cast<const v4i *>(stg + staged<16>(r, c));
+            uint16_t *o = out + (row0 + r) * pitch + col;
+            if (vec) {
+                __builtin_nontemporal_store(v, reinterpret_cast<v4i *>(o));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (col + e < I) o[e] = (uint16_t)((uint32_t)v[e >> 1] >> (16 * (e & 1)));
+            }
+        }
+    };
+    // subtile (i, j)'s four values of this lane as bf16 into a staged tile
+    auto stage_bf16 = [&](uint8_t *stg, int i, int j, const v4f &v) __attribute__((always_inline)) {
+        const int r = wm * TM + 16 * i + l16;
+        const int c = (wn * TH + 16 * j) / 8 + (g4 >> 1);
+        *reinterpret_cast<uint2 *>(stg + staged<16>(r, c) + 8 * (g4 & 1)) =
+            uint2{pack_bf16x2_rne(v.x, v.y), pack_bf16x2_rne(v.z, v.w)};
+    };
+    if (p.gu) {                                    // uniform
+        static_for<SM>([&](auto ic) __attribute__((always_inline)) {
+            static_for<SH>([&](auto jc) __attribute__((always_inline)) {
+                constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
+                stage_bf16(stage0, i, j, acc[i][j]);
+                stage_bf16(stage1, i, j, acc[i][j + SH]);
+            });
+        });
+        lds_barrier();
+        store_bf16(stage0, p.gu, 2 * (int64_t)I);
+        store_bf16(stage1, p.gu + I, 2 * (int64_t)I);
+        lds_barrier();
+    }
+    // h = act(gate) * up, into the gate's registers
+    if (p.act == kActSilu) {
+        static_for<SM>([&](auto ic) __attribute__((always_inline)) {
+            static_for<SH>([&](auto jc) __attribute__((always_inline)) {
+                constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
+                const v4f g = acc[i][j], u = acc[i][j + SH];
+                acc[i][j] = v4f{act_value<kActSilu>(g.x) * u.x, act_value<kActSilu>(g.y) * u.y,
+                                act_value<kActSilu>(g.z) * u.z, act_value<kActSilu>(g.w) * u.w};
+            });
+        });
+    } else {
+        static_for<SM>([&](auto ic) __attribute__((always_inline)) {
+            static_for<SH>([&](auto jc) __attribute__((always_inline)) {
+                constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
+                const v4f g = acc[i][j], u = acc[i][j + SH];
+                acc[i][j] = v4f{act_value<kActGelu>(g.x) * u.x, act_value<kActGelu>(g.y) * u.y,
+                                act_value<kActGelu>(g.z) * u.z, act_value<kActGelu>(g.w) * u.w};
+            });
+        });
+    }
+    if (p.h) {                                     // uniform
+        static_for<SM>([&](auto ic) __attribute__((always_inline)) {
+            static_for<SH>([&](auto jc) __attribute__((always_inline)) {
+                constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
+                stage_bf16(stage0, i, j, acc[i][j]);
+            });
+        });
+        lds_barrier();
+        store_bf16(stage0, p.h, I);
+    }
+    if (p.q) {                                     // uniform; I is a multiple of 128
+        // the row's maximum over this wave's TH columns, then over the waves
+        static_for<SM>([&](auto ic) __attribute__((always_inline)) {
+            constexpr int i = decltype(ic)::value;
+            float m = 0.f;
+            static_for<SH>([&](auto jc) __attribute__((always_inline)) {
+                const v4f v = acc[i][decltype(jc)::value];
+                m = fmaxf(m, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+            });
+            m = fmaxf(m, __shfl_xor(m, 16));
+            m = fmaxf(m, __shfl_xor(m, 32));
+            if (g4 == 0) row_max[wn][wm * TM + 16 * i + l16] = m;
+        });
+        lds_barrier();
+        static_for<SM>([&](auto ic) __attribute__((always_inline)) {
+            constexpr int i = decltype(ic)::value;
+            const int r = wm * TM + 16 * i + l16;
+            float m = row_max[0][r];
+#pragma unroll
+            for (int x = 1; x < WGN; ++x) m = fmaxf(m, row_max[x][r]);
+            const float s = block_scale<PK>(m);
+            const float inv = 1.0f / s;
+            const double y = 1.0 / (double)s;
+            static_for<SH>([&](auto jc) __attribute__((always_inline)) {
+                constexpr int j = decltype(jc)::value;
+                *reinterpret_cast<uint32_t *>(stage1 + staged<8>(r, wn * SH + j) + 4 * g4) =
+                    encode_block4<PK>(acc[i][j], inv, y);
+            });
+            if (wn == 0 && g4 == 0 && row_ok(r)) {
+                const int nb = n0 / 128;
+                if constexpr (PK) {
+                    // byte nb % 4 of the row's word; the last block clears the bytes past it
+                    uint8_t *w = static_cast<uint8_t *>(p.sf) + (sf_base + (int64_t)(nb / 4) * p.ld_sf + m0 + r) * 4;
+                    w[nb & 3] = (uint8_t)(__float_as_uint(s) >> 23);
+                    if (nb == nnb - 1)
+                        for (int e = (nb & 3) + 1; e < 4; ++e) w[e] = 0;
+                } else {
+                    static_cast<float *>(p.sf)[sf_base + (int64_t)nb * p.ld_sf + m0 + r] = s;
+                }
+            }
+        });
+        lds_barrier();
+        for (int item = tid; item < BM * 8; item += 64 * NW) {
+            const int r = item >> 3, c = item & 7;
+            if (row_ok(r))
+                *reinterpret_cast<v4i *>(p.q + (row0 + r) * I + n0 + 16 * c) =
+                    *reinterpret_cast<const v4i *>(stage1 + staged<8>(r, c));
+        }
+    }
+}
+
+template <int BM, int WGM, int WGN, int NST, Mode MODE, bool PK>
+static hipError_t launch_t(const GatedProblem &p, hipStream_t stream, std::string &config) {
+    GatedArgs k{p.a, p.sfa, p.b, p.sfb, p.idx, p.gu, p.h, p.q, p.sf, p.rows_a, p.I, p.K, p.ld_sfa, p.ld_sf, p.G, p.act,
+                0, 0, 4};
+    k.tiles_m = (p.rows_a + BM - 1) / BM;
+    // contiguous 256-row units: at most one per 256 rows plus one per expert segment
+    if (MODE == Mode::Contig && BM == 256) k.tiles_m = p.rows_a / 256 + p.G + 1;
+    k.tiles_n = (p.I + 127) / 128;
+    const int64_t grid = (int64_t)k.tiles_m * k.tiles_n * (MODE == Mode::Masked ? p.G : 1);
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    char buf[160];
+    snprintf(buf, sizeof buf, "family=gated mode=%d tile=%dx%dx128 waves=%dx%d stages=%d grid=%lld%s", (int)MODE, BM,
+             256, WGM, WGN, NST, (long long)grid, PK ? " scales=ue8m0_packed" : "");
+    config = buf;
+    hipLaunchKernelGGL((gated_kernel<BM, WGM, WGN, NST, MODE, PK>), dim3((unsigned)grid), dim3(64 * WGM * WGN), 0,
+                       stream, k);
+    return hipGetLastError();
+}
+
+template <bool PK>
+static hipError_t launch_pk(const GatedProblem &p, hipStream_t stream, std::string &config) {
+    switch (p.mode) {
+    case Mode::Dense:
+        if (p.rows_a >= 256) return launch_t<256, 2, 4, 2, Mode::Dense, PK>(p, stream, config);
+        return launch_t<128, 2, 4, 3, Mode::Dense, PK>(p, stream, config);
+    case Mode::Contig:
+        if (p.rows_a >= 256) return launch_t<256, 2, 4, 2, Mode::Contig, PK>(p, stream, config);
+        return launch_t<128, 2, 4, 3, Mode::Contig, PK>(p, stream, config);
+    case Mode::Masked: return launch_t<128, 2, 4, 3, Mode::Masked, PK>(p, stream, config);
+    case Mode::KGrouped: break;
+    }
+    return hipErrorInvalidValue;
+}
+
+size_t gated_workspace(int M, int I, int K, int num_cus) {
+    (void)M, (void)I, (void)K, (void)num_cus;
+    return 0;
+}
+
+hipError_t launch_gated(const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config) {
+    (void)num_cus;
+    return p.packed ? launch_pk<true>(p, stream, config) : launch_pk<false>(p, stream, config);
+}
+
+}  // namespace dg
