@@ -520,12 +520,14 @@ int64_t dg_get_rmsnorm_backward_workspace_size(int rows, int K);
  * The _ue8m0_packed form takes packed power-of-two scales (sfa
  * [ceil(K/512)][ld_sfa], sfb [2][ceil(I/128)][ceil(K/512)]) and writes such
  * scales (sf [ceil(I/512)][ld_sf]), as dg_fp8_gemm_nt_ue8m0_packed takes them.
- *   workspace: as for dg_fp8_gemm_nt_ws (zeroed once by the caller, left with
- *   its counters zero), dg_get_gated_workspace_size(M, I, K) bytes; NULL, or a
- *   size of 0, runs without splitting the work of small M any further.
+ *   workspace: dg_get_gated_workspace_size(M, I, K) bytes of device memory,
+ *   16-byte aligned, of any content, for a q output at small M (0 bytes
+ *   elsewhere); calls that may run at the same time need one each.  With NULL,
+ *   or too few bytes, a kernel that needs none (and is slower there) computes
+ *   the same outputs.
  * Errors: DG_ERR_NULL; DG_ERR_SHAPE (M < 0; I < 1; K < 128 or K % 128; q with
- * I % 128; 2*I*K or the bytes of sfa reaching 2^31); DG_ERR_ARG (act; a
- * workspace that is too small); DG_ERR_ALIGN.
+ * I % 128; 2*I*K or the bytes of sfa reaching 2^31); DG_ERR_ARG (act);
+ * DG_ERR_ALIGN.
  */
 int dg_fp8_gated_gemm_nt(const uint8_t *a, const float *sfa, int ld_sfa,
                          const uint8_t *b, const float *sfb, int act,

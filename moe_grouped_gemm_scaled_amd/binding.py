@@ -484,11 +484,17 @@ def _call(name, *args):
         raise DGError(status, name)
 
 
+# the current stream's handle without making a torch.cuda.Stream object (2.7 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _queue(t):
     """The current stream of a tensor's device, which has to be the current device (kernels run there)."""
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"tensors on device {t.get_device()}, but the current device is {torch.cuda.current_device()}")
-    return torch.cuda.current_stream().cuda_stream
+    index = t.get_device()
+    if index != torch.cuda.current_device():
+        raise ValueError(f"tensors on device {index}, but the current device is {torch.cuda.current_device()}")
+    return _raw_stream(index)
 
 
 def _sf_rows(scales, kblocks):
@@ -573,19 +579,11 @@ def rmsnorm_backward(dy, h, weight, eps=1e-6, dres=None, dx=None, dw=None, works
 
 
 def get_gated_workspace_size(M: int, I: int, K: int) -> int:
-    """Bytes of scratch fp8_gated_gemm_nt can use on the current device (0: none)."""
+    """Bytes of scratch (of any content) fp8_gated_gemm_nt uses for a quantised output on the current device (0: none)."""
     v = lib().dg_get_gated_workspace_size(int(M), int(I), int(K))
     if v < 0:
         raise DGError(int(v), "dg_get_gated_workspace_size")
     return int(v)
-
-
-def get_gated_workspace(M: int, I: int, K: int, device=None):
-    """A zero-filled uint8 device tensor of get_gated_workspace_size(M, I, K) bytes (None when that is 0).  It may
-    serve any number of fp8_gated_gemm_nt calls in stream order; calls that can run at the same time each need
-    their own."""
-    n = get_gated_workspace_size(M, I, K)
-    return torch.zeros(n, dtype=torch.uint8, device=device if device is not None else "cuda") if n else None
 
 
 def _gated_args(a, sfa, b, sfb, act, h, q, sf, gu, lead, G, rows, ld):
@@ -621,20 +619,22 @@ def fp8_gated_gemm_nt(a, sfa, b, sfb, act="silu", h=None, q=None, sf=None, gu=No
     """h = act(A Wg^T) * (A Wu^T) in one kernel (dg_fp8_gated_gemm_nt): a[M, K], sfa[K/128, ld], b[2, I, K] (Wg, Wu),
     sfb[2, ceil(I/128), K/128]; int32 sfa and sfb are packed power-of-two scales (dg_fp8_gated_gemm_nt_ue8m0_packed).
     act "silu" or "gelu" (tanh form).  Outputs: a tensor to fill, or True for a new one: h[M, I] bf16 (the default),
-    q[M, I] E4M3 with sf[I/128 (packed: ceil(I/512)), ld], gu[M, 2I] bf16 (gate, up).  workspace as for fp8_gemm_nt,
-    from get_gated_workspace().  Returns (h, q, sf, gu), None where not asked for."""
+    q[M, I] E4M3 with sf[I/128 (packed: ceil(I/512)), ld], gu[M, 2I] bf16 (gate, up).  workspace (used for q at small M): a
+    uint8 device tensor of get_gated_workspace_size(M, I, K) bytes, None for none, or "auto".  Returns (h, q, sf, gu), None where not asked for."""
     if a.dim() != 2 or b.dim() != 3 or sfa.dim() != 2:
         raise ValueError("a[M, K], sfa[K/128, ld], b[2, I, K]")
     M = a.shape[0]
     ld = sfa.shape[1]
     ins, act_id, outs, ret, I, K, suffix = _gated_args(a, sfa, b, sfb, act, h, q, sf, gu, (), (), M, ld)
+    stream = _queue(a)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError(f"workspace {workspace!r}")
-        workspace = get_gated_workspace(M, I, K, a.device)
+        n = get_gated_workspace_size(M, I, K) if ret[1] is not None else 0
+        workspace = torch.empty(n, dtype=torch.uint8, device=a.device) if n else None
     _call("dg_fp8_gated_gemm_nt" + suffix, ins[0], ins[1], ld, ins[2], ins[3], act_id, *outs, ld, M, I, K,
           None if workspace is None else _raw(workspace, torch.uint8, workspace.shape, "workspace"),
-          0 if workspace is None else workspace.numel(), _queue(a))
+          0 if workspace is None else workspace.numel(), stream)
     return ret
 
 

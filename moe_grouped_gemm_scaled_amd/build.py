@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdg.so")
 SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "decode.hip", "pipelined.hip", "persistent.hip", "mqa.hip", "noalloc.hip", "stream.hip",
-           "layer_api.cpp", "norm.hip", "gated.hip", "gated_bwd.hip"]
+           "layer_api.cpp", "norm.hip", "gated.hip", "gated_small.hip", "gated_bwd.hip"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: no v_pk_{add,mul,fma}_f32 from the compiler.

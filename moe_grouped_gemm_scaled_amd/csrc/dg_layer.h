@@ -71,8 +71,16 @@ struct GatedProblem {
     size_t ws_bytes;
 };
 // Needs rows_a >= 1 and 2 * I * K and the bytes of sfa below 2^31 per group.
-size_t gated_workspace(int M, int I, int K, int num_cus);
 hipError_t launch_gated(const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config);
+
+// Its kernel for few rows (dense): takes the problem or not (a quantised
+// output needs scratch of gated_small_workspace bytes).
+bool gated_small_takes(const GatedProblem &p, int num_cus);
+size_t gated_small_workspace(int M, int I, int K, int num_cus);
+hipError_t launch_gated_small(const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config);
+
+// Scratch bytes a dense problem with a quantised output can use.
+size_t gated_workspace(int M, int I, int K, int num_cus);
 
 struct GatedBwdProblem {
     const uint16_t *gu, *dh;

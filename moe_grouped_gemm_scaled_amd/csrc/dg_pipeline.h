@@ -57,6 +57,19 @@ __device__ __forceinline__ void dma_lds16(__amdgpu_buffer_rsrc_t r, uint8_t *dst
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, DG_LDS(dst), 16, voffset, soffset, 0, 0);
 }
 
+// One 4-byte-per-lane buffer load into LDS (256 B per wave at `dst`).
+__device__ __forceinline__ void dma_lds4(__amdgpu_buffer_rsrc_t r, uint8_t *dst, int voffset, int soffset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, DG_LDS(dst), 4, voffset, soffset, 0, 0);
+}
+
+// Waits for this wave's LDS reads, so that a DMA may overwrite what they
+// read; a stage that only one wave uses needs no barrier besides.
+__device__ __forceinline__ void lds_reads_done() {
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // MFMA fragment of an operand stored MN-major in LDS: rows are K (PITCH
 // bytes each, 16-byte columns XOR-swizzled by (row & 7)), columns are M (or
 // N).  gfx950's ds_read_b64_tr_b8 gathers, in each group of 16 lanes, byte

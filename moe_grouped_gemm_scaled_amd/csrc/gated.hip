@@ -450,13 +450,10 @@ static hipError_t launch_pk(const GatedProblem &p, hipStream_t stream, std::stri
     return hipErrorInvalidValue;
 }
 
-size_t gated_workspace(int M, int I, int K, int num_cus) {
-    (void)M, (void)I, (void)K, (void)num_cus;
-    return 0;
-}
+size_t gated_workspace(int M, int I, int K, int num_cus) { return gated_small_workspace(M, I, K, num_cus); }
 
 hipError_t launch_gated(const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config) {
-    (void)num_cus;
+    if (gated_small_takes(p, num_cus)) return launch_gated_small(p, num_cus, stream, config);
     return p.packed ? launch_pk<true>(p, stream, config) : launch_pk<false>(p, stream, config);
 }
 

@@ -280,8 +280,8 @@ def test_workspace_reuse_streams_and_graph():
         p = problem((), M, I, K, M + K, packed)
         cases.append((operands(p, packed), M, I, K, packed, p))
     size = max(dg.get_gated_workspace_size(M, I, K) for _, M, I, K, _, _ in cases)
-    ws = torch.zeros(max(size, 16), dtype=torch.uint8, device="cuda")
-    ws2 = torch.zeros_like(ws)
+    ws = torch.full((max(size, 16),), 0xFF, dtype=torch.uint8, device="cuda")      # NaN everywhere: any content will do
+    ws2 = ws.clone()
 
     def call(c, w):
         ops, M, I, K, packed, _ = c
