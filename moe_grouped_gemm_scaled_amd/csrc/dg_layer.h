@@ -96,6 +96,6 @@ struct GatedBwdProblem {
     bool ue8m0;
 };
 // Needs rows >= 1, I a multiple of 128.
-hipError_t launch_gated_bwd(const GatedBwdProblem &p, hipStream_t stream);
+hipError_t launch_gated_bwd(const GatedBwdProblem &p, int num_cus, hipStream_t stream);
 
 }  // namespace dg

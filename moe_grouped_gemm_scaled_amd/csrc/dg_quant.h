@@ -49,4 +49,33 @@ __device__ __forceinline__ float block_scale(float amax) {
     return __uint_as_float((u & 0x7fffffu) ? (u & 0x7f800000u) + 0x00800000u : u);
 }
 
+// Division by a block's scale in fp32 only, for kernels whose arithmetic shows
+// beside their memory time: x / s rounded to fp32 as
+//     q0 = RN(x y),  e = q0 s - x,  q = RN(q0 - e y)   with y = RN(1 / s).
+// e is exact (one fma), and then q is the IEEE quotient (Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990): y is
+// correctly rounded and q0 within an ulp of the quotient.  Subnormal
+// intermediates may break that only for quotients that encode as zero.
+// In this form e = +0 for x = +-0 leaves the sign of the zero.  Power-of-two
+// scales: x y is exact.  An infinite scale (y = 0) counts as 0 in e, which keeps
+// 0 for finite x and NaN for infinities.
+struct BlockDivisor {
+    float y, s;
+};
+template <bool UE8M0>
+__device__ __forceinline__ BlockDivisor block_divisor(float s) {
+    const float y = 1.0f / s;                             // IEEE division (no fast-math)
+    return {y, y == 0.f ? 0.f : s};
+}
+template <bool UE8M0>
+__device__ __forceinline__ float divide(float x, const BlockDivisor &d) {
+    const float q0 = x * d.y;
+    if constexpr (UE8M0) return q0;
+    return __builtin_fmaf(-__builtin_fmaf(q0, d.s, -x), d.y, q0);
+}
+template <bool UE8M0>
+__device__ __forceinline__ uint32_t encode4(const v4f &v, const BlockDivisor &d) {
+    return e4m3_encode4(divide<UE8M0>(v.x, d), divide<UE8M0>(v.y, d), divide<UE8M0>(v.z, d), divide<UE8M0>(v.w, d));
+}
+
 }  // namespace dg

@@ -66,7 +66,7 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
 // without LDS traffic.
 template <int N>
 __device__ __forceinline__ float ror16(float x) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + N, 0xf, 0xf, false));
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x120 + N, 0xf, 0xf, true));
 }
 // NaN operands are left out by fmaxf
 __device__ __forceinline__ float max16(float x) {

@@ -386,12 +386,11 @@ gated_kernel(GatedArgs p) {
 #pragma unroll
             for (int x = 1; x < WGN; ++x) m = fmaxf(m, row_max[x][r]);
             const float s = block_scale<PK>(m);
-            const float inv = 1.0f / s;
-            const double y = 1.0 / (double)s;
+            const BlockDivisor d = block_divisor<PK>(s);
             static_for<SH>([&](auto jc) __attribute__((always_inline)) {
                 constexpr int j = decltype(jc)::value;
                 *reinterpret_cast<uint32_t *>(stage1 + staged<8>(r, wn * SH + j) + 4 * g4) =
-                    encode_block4<PK>(acc[i][j], inv, y);
+                    encode4<PK>(acc[i][j], d);
             });
             if (wn == 0 && g4 == 0 && row_ok(r)) {
                 const int nb = n0 / 128;

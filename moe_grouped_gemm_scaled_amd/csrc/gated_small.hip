@@ -272,12 +272,10 @@ __global__ void __launch_bounds__(64) gated_finish_kernel(GatedSmallArgs p) {
     if (p.h && in) store8(p.h + (int64_t)row * I + c, h);
     if (!p.q) return;                                 // uniform; I is a multiple of 128
     const float s = block_scale<PK>(max16(m));
-    const float inv = 1.0f / s;
-    const double y = 1.0 / (double)s;
+    const BlockDivisor d = block_divisor<PK>(s);
     if (in)
         *reinterpret_cast<uint2 *>(p.q + (int64_t)row * I + c) =
-            uint2{encode_block4<PK>(v4f{h[0], h[1], h[2], h[3]}, inv, y),
-                  encode_block4<PK>(v4f{h[4], h[5], h[6], h[7]}, inv, y)};
+            uint2{encode4<PK>(v4f{h[0], h[1], h[2], h[3]}, d), encode4<PK>(v4f{h[4], h[5], h[6], h[7]}, d)};
     if (in && (lane & 15) == 0) {
         if constexpr (PK) {
             // byte nb % 4 of the row's word; the last block clears the bytes past it

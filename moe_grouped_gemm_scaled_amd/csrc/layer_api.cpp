@@ -132,7 +132,7 @@ int gated_bwd_impl(const uint16_t *gu, const uint16_t *dh, int act, const int32_
     const int st = dg::current_device_cus(cus);
     if (st != DG_OK) return st;
     const dg::GatedBwdProblem p{gu, dh, m_indices, dgu, q, sf, qt, sft, ht, sfht, rows, I, ld_sf, act, ue8m0};
-    return status(dg::launch_gated_bwd(p, static_cast<hipStream_t>(stream)));
+    return status(dg::launch_gated_bwd(p, cus, static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace

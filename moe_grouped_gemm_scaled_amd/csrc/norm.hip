@@ -111,15 +111,14 @@ rmsnorm_quant_kernel(NormFwdArgs p) {
         if (p.y && in) store8<true>(p.y + (int64_t)row * K + col[c], y);
         if (p.q) {                                     // uniform
             const float s = p.format == kSfFp32 ? block_scale<false>(amax) : block_scale<true>(amax);
+            const v4f lo = v4f{y[0], y[1], y[2], y[3]}, hi = v4f{y[4], y[5], y[6], y[7]};
             uint2 w;
             if (p.format == kSfFp32) {
-                const double inv = 1.0 / (double)s;
-                w.x = encode_block4<false>(v4f{y[0], y[1], y[2], y[3]}, 0.f, inv);
-                w.y = encode_block4<false>(v4f{y[4], y[5], y[6], y[7]}, 0.f, inv);
+                const BlockDivisor d = block_divisor<false>(s);
+                w = uint2{encode4<false>(lo, d), encode4<false>(hi, d)};
             } else {
-                const float inv = 1.0f / s;
-                w.x = encode_block4<true>(v4f{y[0], y[1], y[2], y[3]}, inv, 0.0);
-                w.y = encode_block4<true>(v4f{y[4], y[5], y[6], y[7]}, inv, 0.0);
+                const BlockDivisor d = block_divisor<true>(s);
+                w = uint2{encode4<true>(lo, d), encode4<true>(hi, d)};
             }
             if (in) *reinterpret_cast<uint2 *>(p.q + (int64_t)row * K + col[c]) = w;
             if (p.format == kSfPacked) {
