@@ -446,15 +446,16 @@ def _raw(t, dtype, shape, name):
     """The address of a dense device tensor of this type (one of a tuple, or any when None) and shape; None for None."""
     if t is None:
         return None
-    if dtype is not None and t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
+    typed = dtype is None or t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)
+    if typed and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    if not typed:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a device tensor")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name}: must be contiguous")
 
 
 def _type_of(t, name):

@@ -69,6 +69,7 @@ struct GatedProblem {
     bool packed;
     void *ws;          // caller's scratch (dense), or NULL
     size_t ws_bytes;
+    int row0 = 0;      // rows of the caller's problem before `a` (set by the launcher that cuts it)
 };
 // Needs rows_a >= 1 and 2 * I * K and the bytes of sfa below 2^31 per group.
 hipError_t launch_gated(const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config);

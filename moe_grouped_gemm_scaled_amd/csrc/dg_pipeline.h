@@ -148,6 +148,41 @@ __device__ __forceinline__ int contig_unit_block(const int32_t *idx, int nblocks
     return -1;
 }
 
+// The same walk to its end: returns the first block of unit u (-1 for none, or
+// u < 0) and leaves the number of units in `units`.
+__device__ __forceinline__ int contig_scan(const int32_t *idx, int nblocks, int u, int &units) {
+    const int lane = threadIdx.x & 63;
+    int prev_e = -1;     // expert of the block before this round (none: -1)
+    int seg = -1;        // first block of the segment running into this round
+    int count = 0, found = -1;
+    for (int base = 0; base < nblocks; base += 64) {
+        const int b = base + lane;
+        const int e = b < nblocks ? idx[(int64_t)b * 128] : -1;
+        int ep = __shfl_up(e, 1);
+        if (lane == 0) ep = prev_e;
+        int sg = e >= 0 && e != ep ? b : -1;      // inclusive max-scan of segment starts
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int t = __shfl_up(sg, o);
+            if (lane >= o) sg = sg > t ? sg : t;
+        }
+        sg = sg > seg ? sg : seg;
+        const bool unit = e >= 0 && ((b - sg) & 1) == 0;
+        const uint64_t m = __ballot(unit);
+        const int n = __popcll(m);
+        if (u >= count && u < count + n) {
+            const int rank = __popcll(m & ((1ull << lane) - 1ull));
+            const uint64_t hit = __ballot(unit && rank == u - count);
+            found = base + __ffsll((unsigned long long)hit) - 1;
+        }
+        count += n;
+        prev_e = __shfl(e, 63);
+        seg = __shfl(sg, 63);
+    }
+    units = count;
+    return found;
+}
+
 // Steps U, U+1, .. of one round of the K loop, step U + i running only when
 // b + U + i < n.  Nested (not sequential) conditions: the control flow then
 // has no path that skips a step and runs a later one, so the compiler's count

@@ -40,7 +40,23 @@ struct GatedArgs {
     void *sf;
     int rows_a, I, K, ld_sfa, ld_sf, G, act;
     int tiles_m, tiles_n, gm;
+    int part, cus;             // contiguous: which rows this launch takes (ContigPart)
+    int sa_cols;               // columns of sfa from the first row on (ld_sfa, less the rows before it)
 };
+
+// The contiguous layout can take two launches: 256-row units that fill the CUs
+// a whole number of times, then the remaining rows in 128-row blocks, when
+// those fit the CUs at once: a last, partly filled round of 256-row tiles costs
+// as much as a full one.  How many units there are is known on the device
+// only, so both launches work it out from m_indices.
+enum ContigPart : int { kAllRows = 0, kHead = 1, kTail = 2 };
+
+// Units of the head launch: all `units`, or those of the full rounds.
+__device__ __forceinline__ int head_units(int units, int tiles_n, int cus) {
+    const int64_t tiles = (int64_t)units * tiles_n;
+    const int full = (int)(tiles / cus * cus / tiles_n);
+    return 2 * (int64_t)(units - full) * tiles_n <= cus ? full : units;
+}
 
 // 16-byte chunk c of row r in a staged output tile of CPR chunks per row: the
 // chunk index is XORed with the row, so that the 16 rows that a wave writes
@@ -67,7 +83,7 @@ gated_kernel(GatedArgs p) {
     constexpr int STAGE = OFF_JUNK + 1024;
     constexpr int DA = BM / (8 * NW), DB = BN / (8 * NW);   // 1-KB LDS-DMA chunks per wave per K block
     constexpr int PER_BLOCK = DA + DB + 1;
-    static_assert(NST >= 2 && NST <= 3 && NST * STAGE + BM * WGN * 4 <= 160 * 1024, "LDS");
+    static_assert(NST >= 2 && NST <= 3 && NST * STAGE + BM * (WGN * 4 + 1) <= 160 * 1024, "LDS");
     static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM / 4 <= 64 && NW >= 2, "DMA chunks");
     static_assert((NST - 2) * PER_BLOCK < 64, "vmcnt immediate");
     static_assert(TH % 16 == 0 && BM * 256 <= STAGE, "a staged output tile fits one stage");
@@ -88,17 +104,40 @@ gated_kernel(GatedArgs p) {
     const int nnb = (I + 127) / 128;
     const int nkw = PK ? (nkb + 3) / 4 : nkb;
     const int tiles_per_group = p.tiles_m * p.tiles_n;
-    int t_lin = xcd_remap(blockIdx.x, gridDim.x);
+    // contiguous: the first row block and the number of row tiles of this launch
+    int tiles_m = p.tiles_m, block0 = 0;
+    if constexpr (MODE == Mode::Contig) {
+        const int nblocks = p.rows_a / 128;
+        if (p.part != kAllRows) {
+            int units = 0;
+            contig_scan(p.idx, nblocks, -1, units);
+            const int head = head_units(units, p.tiles_n, p.cus);
+            if (BM == 256) {
+                tiles_m = head;
+            } else {
+                if (head >= units) return;         // no tail: uniform exit
+                int u = 0;
+                block0 = head > 0 ? contig_scan(p.idx, nblocks, head, u) : 0;
+                tiles_m = (nblocks - block0) * 128 / BM;
+            }
+        }
+        tiles_m = __builtin_amdgcn_readfirstlane(tiles_m);
+        block0 = __builtin_amdgcn_readfirstlane(block0);
+    }
+    const int total = MODE == Mode::Contig ? tiles_m * p.tiles_n : (int)gridDim.x;
+    if ((int)blockIdx.x >= total) return;          // uniform exit
+    int t_lin = xcd_remap(blockIdx.x, total);
     int grp = 0;
     if (MODE == Mode::Masked) {
         grp = t_lin / tiles_per_group;
         t_lin -= grp * tiles_per_group;
     }
     int tm, tn;
-    raster(t_lin, p.tiles_m, p.tiles_n, p.gm, tm, tn);
-    int m0 = tm * BM;
+    raster(t_lin, tiles_m, p.tiles_n, p.gm, tm, tn);
+    int m0 = block0 * 128 + tm * BM;
     if constexpr (MODE == Mode::Contig && BM == 256) {
-        const int ub = __builtin_amdgcn_readfirstlane(contig_unit_block(p.idx, p.rows_a / 128, tm));
+        int units = 0;
+        const int ub = __builtin_amdgcn_readfirstlane(contig_scan(p.idx, p.rows_a / 128, tm, units));
         if (ub < 0) return;                        // no such unit: uniform exit
         m0 = ub * 128;
     }
@@ -141,6 +180,8 @@ gated_kernel(GatedArgs p) {
     const int l16 = lane & 15;
     const int g4 = lane >> 4;
     const bool wave_live = wm * TM < rows;         // the wave has rows to multiply
+    int row_id = -1;                               // contiguous: the expert of tile row tid
+    if (MODE == Mode::Contig && tid < rows) row_id = p.idx[m0 + tid];
 
     // ---- DMA plan: chunk c = wave + NW*i holds tile rows 8c .. 8c+7; lane l
     // lands at row +l/8, 16-byte chunk l%8 and fetches chunk (l%8) ^ (l/8).
@@ -170,9 +211,10 @@ gated_kernel(GatedArgs p) {
     // every wave issues the same number
     const bool wsa = wave == 0;
     const __amdgpu_buffer_rsrc_t rS = __builtin_amdgcn_make_buffer_rsrc(
-        wsa ? (void *)SFA : (void *)SFB, (short)0, wsa ? nkw * ld * 4 : 2 * nnb * nkw * 4, 0x00020000);
+        wsa ? (void *)SFA : (void *)SFB, (short)0,
+        wsa ? ((nkw - 1) * ld + p.sa_cols) * 4 : 2 * nnb * nkw * 4, 0x00020000);
     const int sa_row = m0 + 4 * lane;
-    const int v_s = wsa ? (4 * lane < BM && sa_row < ld ? sa_row * 4 : kOutOfRange)
+    const int v_s = wsa ? (4 * lane < BM && sa_row < p.sa_cols ? sa_row * 4 : kOutOfRange)
                         : (wave == 1 && lane < 2 ? (lane * nnb + n0 / 128) * nkw * 4 : kOutOfRange);
     const int lds_s = wsa ? OFF_SA : (wave == 1 ? OFF_SB : OFF_JUNK);
     auto dma = [&](uint8_t *stg, int kb) __attribute__((always_inline)) {
@@ -291,10 +333,15 @@ gated_kernel(GatedArgs p) {
 
     // ---- epilogue.  Row r of the tile is stored when it holds data (its
     // output row is row_base + m0 + r).
+    // Contiguous: a row of the expert, looked up once per row (looked up with
+    // every 16 bytes stored it took 17 us of a 136 us round).
+    __shared__ uint8_t of_expert[MODE == Mode::Contig ? BM : 1];
+    if constexpr (MODE == Mode::Contig) {
+        if (tid < BM) of_expert[tid] = row_id == expert;
+        lds_barrier();
+    }
     auto row_ok = [&](int r) __attribute__((always_inline)) {
-        bool ok = r < rows;
-        if (MODE == Mode::Contig) ok = ok && p.idx[m0 + r] == expert;
-        return ok;
+        return r < rows && (MODE != Mode::Contig || of_expert[r]);
     };
     const int64_t row0 = row_base + m0;
     // staged bf16 tile (256-byte rows) to columns n0 .. n0+127 of out [..][pitch]
@@ -415,35 +462,100 @@ gated_kernel(GatedArgs p) {
     }
 }
 
-template <int BM, int WGM, int WGN, int NST, Mode MODE, bool PK>
-static hipError_t launch_t(const GatedProblem &p, hipStream_t stream, std::string &config) {
+template <int BM, int NST, Mode MODE, bool PK>
+static hipError_t launch_t(const GatedProblem &p, int num_cus, ContigPart part, hipStream_t stream,
+                           std::string &config) {
     GatedArgs k{p.a, p.sfa, p.b, p.sfb, p.idx, p.gu, p.h, p.q, p.sf, p.rows_a, p.I, p.K, p.ld_sfa, p.ld_sf, p.G, p.act,
-                0, 0, 4};
+                0, 0, 4, part, num_cus, p.ld_sfa - p.row0};
     k.tiles_m = (p.rows_a + BM - 1) / BM;
     // contiguous 256-row units: at most one per 256 rows plus one per expert segment
     if (MODE == Mode::Contig && BM == 256) k.tiles_m = p.rows_a / 256 + p.G + 1;
     k.tiles_n = (p.I + 127) / 128;
-    const int64_t grid = (int64_t)k.tiles_m * k.tiles_n * (MODE == Mode::Masked ? p.G : 1);
+    int64_t grid = (int64_t)k.tiles_m * k.tiles_n * (MODE == Mode::Masked ? p.G : 1);
+    if (part == kTail) {
+        // at most half the CUs' worth of 256-row units, two blocks each, and
+        // the padding blocks behind them, which exit
+        k.tiles_m = p.rows_a / BM;
+        grid = (int64_t)k.tiles_m * k.tiles_n;
+    }
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     char buf[160];
-    snprintf(buf, sizeof buf, "family=gated mode=%d tile=%dx%dx128 waves=%dx%d stages=%d grid=%lld%s", (int)MODE, BM,
-             256, WGM, WGN, NST, (long long)grid, PK ? " scales=ue8m0_packed" : "");
-    config = buf;
-    hipLaunchKernelGGL((gated_kernel<BM, WGM, WGN, NST, MODE, PK>), dim3((unsigned)grid), dim3(64 * WGM * WGN), 0,
-                       stream, k);
+    snprintf(buf, sizeof buf, "%sfamily=gated mode=%d tile=%dx%dx128 waves=2x4 stages=%d grid=%lld%s",
+             config.empty() ? "" : " + ", (int)MODE, BM, 256, NST, (long long)grid, PK ? " scales=ue8m0_packed" : "");
+    config += buf;
+    hipLaunchKernelGGL((gated_kernel<BM, 2, 4, NST, MODE, PK>), dim3((unsigned)grid), dim3(512), 0, stream, k);
     return hipGetLastError();
 }
 
+// Rows of a tile.  A round of tiles over the CUs takes about 100, 60 and 40
+// (measured, K = 7168: 88 to 108, 53 to 60 and 40 us) with 256, 128 and 64 rows:
+// smaller tiles multiply less per byte they load, but fill the CUs where there
+// are few rows.
+static int tile_rows(int rows, int groups, int64_t tiles_n, int num_cus) {
+    int best = 256;
+    int64_t least = INT64_MAX;
+    const int bm[3] = {256, 128, 64}, cost[3] = {100, 60, 40};
+    for (int i = 0; i < 3; ++i) {
+        const int64_t tiles = (int64_t)groups * ((rows + bm[i] - 1) / bm[i]) * tiles_n;
+        const int64_t c = (tiles + num_cus - 1) / num_cus * cost[i];
+        if (c < least) {
+            least = c;
+            best = bm[i];
+        }
+    }
+    return best;
+}
+
+template <Mode MODE, bool PK>
+static hipError_t launch_rows(int rows, const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config) {
+    if (rows == 256) return launch_t<256, 2, MODE, PK>(p, num_cus, kAllRows, stream, config);
+    if (rows == 128) return launch_t<128, 3, MODE, PK>(p, num_cus, kAllRows, stream, config);
+    return launch_t<64, 3, MODE, PK>(p, num_cus, kAllRows, stream, config);
+}
+
 template <bool PK>
-static hipError_t launch_pk(const GatedProblem &p, hipStream_t stream, std::string &config) {
+static hipError_t launch_pk(const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config) {
+    const int64_t tiles_n = (p.I + 127) / 128;
     switch (p.mode) {
-    case Mode::Dense:
-        if (p.rows_a >= 256) return launch_t<256, 2, 4, 2, Mode::Dense, PK>(p, stream, config);
-        return launch_t<128, 2, 4, 3, Mode::Dense, PK>(p, stream, config);
-    case Mode::Contig:
-        if (p.rows_a >= 256) return launch_t<256, 2, 4, 2, Mode::Contig, PK>(p, stream, config);
-        return launch_t<128, 2, 4, 3, Mode::Contig, PK>(p, stream, config);
-    case Mode::Masked: return launch_t<128, 2, 4, 3, Mode::Masked, PK>(p, stream, config);
+    case Mode::Dense: {
+        // full rounds of 256-row tiles, then the rows that are left in tiles of
+        // their own choice (4500 rows: 16 row tiles of 256, then 64-row tiles)
+        const int64_t row_tiles = p.rows_a / 256, full = row_tiles * tiles_n / num_cus * num_cus / tiles_n;
+        const int head = (int)(full * 256), rest = p.rows_a - head;
+        if (head > 0) {
+            GatedProblem q = p;
+            q.rows_a = head;
+            const hipError_t err = launch_t<256, 2, Mode::Dense, PK>(q, num_cus, kAllRows, stream, config);
+            if (err != hipSuccess || rest == 0) return err;
+        }
+        GatedProblem q = p;
+        q.rows_a = rest;
+        q.row0 = head;
+        q.a += (int64_t)head * p.K;
+        q.sfa += head;
+        if (q.gu) q.gu += (int64_t)head * 2 * p.I;
+        if (q.h) q.h += (int64_t)head * p.I;
+        if (q.q) {
+            q.q += (int64_t)head * p.I;
+            q.sf = static_cast<uint32_t *>(p.sf) + head;
+        }
+        return launch_rows<Mode::Dense, PK>(tile_rows(rest, 1, tiles_n, num_cus), q, num_cus, stream, config);
+    }
+    case Mode::Contig: {
+        // every expert's last unit may hold one block only: one more 256-row tile each
+        const int rows = tile_rows(p.rows_a + 128 * p.G, 1, tiles_n, num_cus);
+        if (rows == 64 || p.rows_a < 256) return launch_rows<Mode::Contig, PK>(rows == 256 ? 128 : rows, p, num_cus, stream, config);
+        if (rows == 128 && p.rows_a / 128 * tiles_n <= num_cus)
+            return launch_rows<Mode::Contig, PK>(128, p, num_cus, stream, config);
+        const hipError_t err = launch_t<256, 2, Mode::Contig, PK>(p, num_cus, kHead, stream, config);
+        if (err != hipSuccess) return err;
+        return launch_t<128, 3, Mode::Contig, PK>(p, num_cus, kTail, stream, config);
+    }
+    case Mode::Masked: {
+        // the groups' counts are on the device: the caller's hint, or the capacity
+        const int expect = p.expected_m > 0 && p.expected_m < p.rows_a ? p.expected_m : p.rows_a;
+        return launch_rows<Mode::Masked, PK>(tile_rows(expect, p.G, tiles_n, num_cus), p, num_cus, stream, config);
+    }
     case Mode::KGrouped: break;
     }
     return hipErrorInvalidValue;
@@ -453,7 +565,7 @@ size_t gated_workspace(int M, int I, int K, int num_cus) { return gated_small_wo
 
 hipError_t launch_gated(const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config) {
     if (gated_small_takes(p, num_cus)) return launch_gated_small(p, num_cus, stream, config);
-    return p.packed ? launch_pk<true>(p, stream, config) : launch_pk<false>(p, stream, config);
+    return p.packed ? launch_pk<true>(p, num_cus, stream, config) : launch_pk<false>(p, num_cus, stream, config);
 }
 
 }  // namespace dg

@@ -143,25 +143,20 @@ static hipError_t launch_fwd_t(const NormFwdArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Waves per row: one when the rows alone give every SIMD work (then no
-// barrier stands in the way of a row), four or sixteen otherwise, so that a
-// row's latency shrinks; long rows need them for their registers.
+// Waves per row: one up to 1024 columns (16384 rows: 14 against 25 us with
+// four at 512 columns, 22 against 27 at 1024), four from there (4096 rows of
+// 7168: 40.7 us, 5.1 TB/s, against 47 us with one; nontemporal loads and
+// stores: 45.4 us without), sixteen for few long rows, where a row's latency is
+// the call's.
 template <typename TX, typename TR, typename TW>
 static hipError_t launch_fwd_k(const NormFwdArgs &a, hipStream_t stream) {
     const int n = (a.K + 511) / 512;                   // 512-column chunks
-    if (n <= 16 && a.rows >= 2048) {
-        if (n <= 2) return launch_fwd_t<TX, TR, TW, 1, 2>(a, stream);
-        if (n <= 4) return launch_fwd_t<TX, TR, TW, 1, 4>(a, stream);
-        if (n <= 8) return launch_fwd_t<TX, TR, TW, 1, 8>(a, stream);
-        if (n <= 12) return launch_fwd_t<TX, TR, TW, 1, 12>(a, stream);
-        return launch_fwd_t<TX, TR, TW, 1, 16>(a, stream);
-    }
-    if (n <= 4 || (n <= 16 && a.rows >= 512)) {
-        if (n <= 4) return launch_fwd_t<TX, TR, TW, 4, 1>(a, stream);
-        if (n <= 8) return launch_fwd_t<TX, TR, TW, 4, 2>(a, stream);
-        return launch_fwd_t<TX, TR, TW, 4, 4>(a, stream);
-    }
-    if (n <= 16) return launch_fwd_t<TX, TR, TW, 16, 1>(a, stream);
+    if (n <= 1) return launch_fwd_t<TX, TR, TW, 1, 1>(a, stream);
+    if (n <= 2) return launch_fwd_t<TX, TR, TW, 1, 2>(a, stream);
+    if (n <= 4) return launch_fwd_t<TX, TR, TW, 4, 1>(a, stream);
+    if (n <= 16 && a.rows < 512) return launch_fwd_t<TX, TR, TW, 16, 1>(a, stream);
+    if (n <= 8) return launch_fwd_t<TX, TR, TW, 4, 2>(a, stream);
+    if (n <= 16) return launch_fwd_t<TX, TR, TW, 4, 4>(a, stream);
     if (n <= 32) return launch_fwd_t<TX, TR, TW, 16, 2>(a, stream);
     return hipErrorInvalidValue;
 }
@@ -338,11 +333,13 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *__restric
     }
 }
 
-// Workgroups of the backward pass: two per CU at most, each with at least
-// four rows, so that their partial rows of dw stay small next to the rows.
+// Workgroups of the backward pass: two per CU at most, each with two rows or
+// more, so that their partial rows of dw stay small next to the rows (333 rows
+// of 2048: 5.6 us, 7.5 with four rows or more; one row or more changes
+// nothing).
 static int bwd_groups(int rows, int num_cus) {
     const int64_t most = 2 * (int64_t)num_cus;
-    const int64_t g = ((int64_t)rows + 3) / 4;
+    const int64_t g = ((int64_t)rows + 1) / 2;
     return (int)(g < most ? (g > 0 ? g : 1) : most);
 }
 

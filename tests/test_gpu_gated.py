@@ -164,7 +164,10 @@ def test_dense_any_width(M, I, K, packed):
 @pytest.mark.parametrize("counts", [[1], [128, 128], [0, 5, 300, 128, 0, 257], [1000, 1], [129, 3, 130, 500], [0, 0, 7]])
 @pytest.mark.parametrize("packed", [False, True])
 def test_contiguous(counts, packed):
-    I, K = 256, 640
+    check_contiguous(counts, 256, 640, packed)
+
+
+def check_contiguous(counts, I, K, packed):
     announce(f"gated contiguous {counts} packed={packed}")
     idx = synth.contiguous_m_indices(counts)
     M, G = idx.size, len(counts)
@@ -189,6 +192,41 @@ def test_contiguous(counts, packed):
         t = torch.from_numpy(at).cuda()
         check_rows(f"expert {e} of {counts}", o.gu[t], o.h[t], o.q[t], scales_of(o.sf[:, t], packed, I // 128).T, I, gate,
                    up, "silu", packed)
+
+
+@pytest.fixture
+def few_cus():
+    """A cap of 4 CUs: small problems then take several rounds of tiles, as large ones do on all CUs."""
+    dg.set_num_cus(4)
+    yield
+    dg.set_num_cus(0)
+
+
+@pytest.mark.parametrize("M,I,K", [(512, 256, 256), (520, 256, 384), (700, 256, 256), (1030, 128, 256), (1100, 384, 128),
+                                   (900, 1, 128), (1285, 136, 256), (2050, 128, 128), (64, 512, 256), (100, 640, 384)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_dense_in_rounds(M, I, K, packed, few_cus):
+    """Full rounds of large tiles, then the remaining rows in smaller ones."""
+    announce(f"gated rounds M={M} I={I} K={K} packed={packed}")
+    p = problem((), M, I, K, M + I + K, packed)
+    ops = operands(p, packed)
+    ld = p[1].shape[1]
+    quant = I % 128 == 0
+    o = Outputs((), M, I, ld, packed, quant)
+    dg.fp8_gated_gemm_nt(*ops, h=o.h, q=o.q, sf=o.sf, gu=o.gu)
+    torch.cuda.synchronize()
+    o.guards()
+    gate, up = projections(*p)
+    sf = scales_of(o.sf[:, :M], packed, I // 128).T if quant else None
+    check_rows(f"M={M} I={I} {dg.last_config()}", o.gu, o.h, o.q, sf, I, gate, up, "silu", packed)
+
+
+@pytest.mark.parametrize("counts", [[600], [128, 900, 0, 130], [1, 1, 1, 1, 1, 1, 1], [300, 300, 300], [512, 512, 40], [1500, 128],
+                                    [0, 0, 1300, 0, 257]])
+@pytest.mark.parametrize("I", [128, 384])
+@pytest.mark.parametrize("packed", [False, True])
+def test_contiguous_in_rounds(counts, I, packed, few_cus):
+    check_contiguous(counts, I, 256, packed)
 
 
 def test_contiguous_nothing_and_bad_ids():
