@@ -441,28 +441,64 @@ _TYPES = {torch.bfloat16: 0, torch.float32: 1}
 _ACTS = {"silu": 0, "gelu": 1}
 _SUFFIX = {"fp32": "", "ue8m0": "_ue8m0", "ue8m0_packed": "_ue8m0_packed"}
 
+# Type sets of arguments, as the bits that the native checks use.
+_BF16, _F32, _REAL, _E4M3, _I32 = 1, 2, 3, 12, 16
+_BIT_TYPES = {_BF16: torch.bfloat16, _F32: torch.float32, _REAL: (torch.bfloat16, torch.float32), _E4M3: _FP8,
+              _I32: torch.int32}
+
+# the current stream's handle without making a torch.cuda.Stream object (2.7 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+try:
+    from ._args import addresses as _native_addresses   # csrc/py_args.cpp: the checks of _raw, natively
+except ImportError:                                     # not built: the same checks in Python
+    def _native_addresses(*_):
+        return None
+
 
 def _raw(t, dtype, shape, name):
-    """The address of a dense device tensor of this type (one of a tuple, or any when None) and shape; None for None."""
+    """The address of a dense device tensor of this type (or one of a tuple) and shape; None for None."""
     if t is None:
         return None
-    typed = dtype is None or t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)
-    if typed and t.is_cuda and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    if not typed:
+    if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a device tensor")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name}: must be contiguous")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _device(t, name):
+    """The device of a call's tensors, which has to be the current device (kernels run there)."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: must be a device tensor")
+    if index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on device {index}, but the current device is {torch.cuda.current_device()}")
+    return index
+
+
+def _pointers(index, names, *specs):
+    """Addresses of the tensors in specs = t0, types0, shape0, t1, .. (None for None), all checked."""
+    got = _native_addresses(index, *specs)
+    if got is None:
+        got = []
+        for name, t, bits, shape in zip(names, specs[0::3], specs[1::3], specs[2::3]):
+            got.append(_raw(t, _BIT_TYPES[bits], shape, name))
+            if t is not None and t.get_device() != index:
+                raise ValueError(f"{name}: on device {t.get_device()}, other arguments on device {index}")
+    return got
 
 
 def _type_of(t, name):
     try:
         return _TYPES[t.dtype]
-    except KeyError:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float32") from None
+    except (KeyError, AttributeError):
+        raise TypeError(f"{name}: {getattr(t, 'dtype', t)}, expected a tensor of torch.bfloat16 or torch.float32") from None
 
 
 def _act_of(act):
@@ -479,27 +515,23 @@ def _out(t, shape, dtype, device, zero=False):
     return None if t is False else t
 
 
+_functions = {}
+
+
 def _call(name, *args):
-    status = getattr(lib(), name)(*args)
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(lib(), name)
+    status = f(*args)
     if status != DG_OK:
         raise DGError(status, name)
 
 
-# the current stream's handle without making a torch.cuda.Stream object (2.7 us a call)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+def _sf_rows(packed, kblocks):
+    return (kblocks + 3) // 4 if packed else kblocks
 
 
-def _queue(t):
-    """The current stream of a tensor's device, which has to be the current device (kernels run there)."""
-    index = t.get_device()
-    if index != torch.cuda.current_device():
-        raise ValueError(f"tensors on device {index}, but the current device is {torch.cuda.current_device()}")
-    return _raw_stream(index)
-
-
-def _sf_rows(scales, kblocks):
-    return (kblocks + 3) // 4 if scales == "ue8m0_packed" else kblocks
+_NORM_NAMES = ("residual", "weight", "residual_out", "y", "q", "sf")
 
 
 def rmsnorm_quantize_e4m3_1x128(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, q=None, sf=None,
@@ -512,36 +544,43 @@ def rmsnorm_quantize_e4m3_1x128(x, weight, eps=1e-6, residual=None, residual_out
     to fill, or True for a new one; scales "fp32" or "ue8m0" (sf[K/128, ld_sf] fp32) or "ue8m0_packed"
     (sf[ceil(K/512), ld_sf] int32).  q=False leaves the quantised output out (y is needed then).
     Returns (q, sf, residual_out, y), None where not asked for."""
-    if scales not in _SUFFIX:
+    suffix = _SUFFIX.get(scales)
+    if suffix is None:
         raise ValueError(f"scales {scales!r}, expected one of {tuple(_SUFFIX)}")
-    if x.dim() != 2 or not x.is_cuda or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError("x: a device tensor [rows, K] with dense columns")
-    rows, K = x.shape
+    if x.dim() != 2:
+        raise ValueError("x: must have two dimensions, [rows, K]")
     shape = x.shape
+    rows, K = shape
+    pitch, column = x.stride()
+    if column != 1 and K > 1:
+        raise ValueError("x: columns must be dense")
+    index = _device(x, "x")
+    res_type = 0
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
-    elif residual_out is None:
-        residual_out = torch.empty_like(residual)
-    y = _out(y, shape, torch.bfloat16, x.device)
-    sf_t = torch.int32 if scales == "ue8m0_packed" else torch.float32
+    else:
+        res_type = _type_of(residual, "residual")
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+    if y is True:
+        y = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+    packed = scales == "ue8m0_packed"
+    ld, sf_shape = 0, ()
     if q is False:
         q = sf = None
-        ld = 0
     else:
         ld = (sf.shape[-1] if sf is not None else (rows + 3) // 4 * 4) if ld_sf is None else int(ld_sf)
-        n = _sf_rows(scales, K // 128)
+        sf_shape = (_sf_rows(packed, K // 128), ld)
         if q is None:
             q = torch.empty(shape, dtype=torch.uint8, device=x.device)
         if sf is None:
-            sf = torch.zeros((n, ld), dtype=sf_t, device=x.device)
-    _call("dg_rmsnorm_quantize_e4m3_1x128" + _SUFFIX[scales], x.data_ptr(), _type_of(x, "x"),
-          x.stride(0) if rows > 1 else K,
-          _raw(residual, None, shape, "residual"), 0 if residual is None else _type_of(residual, "residual"),
-          _raw(weight, None, (K,), "weight"), _type_of(weight, "weight"), eps,
-          _raw(residual_out, None if residual is None else residual.dtype, shape, "residual_out"),
-          _raw(y, torch.bfloat16, shape, "y"), _raw(q, _FP8, shape, "q"),
-          None if q is None else _raw(sf, sf_t, (n, ld), "sf"), ld, rows, K, _queue(x))
+            sf = torch.zeros(sf_shape, dtype=torch.int32 if packed else torch.float32, device=x.device)
+    res_bits = _F32 if res_type else _BF16
+    p = _pointers(index, _NORM_NAMES, residual, res_bits, shape, weight, _REAL, (K,), residual_out, res_bits, shape,
+                  y, _BF16, shape, q, _E4M3, shape, sf, _I32 if packed else _F32, sf_shape)
+    _call("dg_rmsnorm_quantize_e4m3_1x128" + suffix, x.data_ptr(), _type_of(x, "x"), pitch if rows > 1 else K, p[0],
+          res_type, p[1], _type_of(weight, "weight"), eps, p[2], p[3], p[4], p[5], ld, rows, K, _raw_stream(index))
     return q, sf, residual_out, y
 
 
@@ -553,6 +592,9 @@ def get_rmsnorm_backward_workspace_size(rows: int, K: int) -> int:
     return int(v)
 
 
+_NORM_BWD_NAMES = ("dy", "h", "weight", "dres", "dx", "dw")
+
+
 def rmsnorm_backward(dy, h, weight, eps=1e-6, dres=None, dx=None, dw=None, workspace="auto"):
     """Gradient of the RMS norm (dg_rmsnorm_backward): dy[rows, K] bf16 or fp32, h[rows, K] the norm's input as stored
     (bf16 or fp32), dres[rows, K] of h's type the gradient arriving at h itself (or None); returns (dx of h's type,
@@ -562,21 +604,32 @@ def rmsnorm_backward(dy, h, weight, eps=1e-6, dres=None, dx=None, dw=None, works
     if len(shape) != 2:
         raise ValueError(f"h: shape {tuple(shape)}, expected [rows, K]")
     rows, K = shape
+    if isinstance(workspace, str) and workspace != "auto":
+        raise ValueError(f"workspace {workspace!r}")
+    index = _device(h, "h")
+    h_type = _type_of(h, "h")
     if isinstance(workspace, str):
-        if workspace != "auto":
-            raise ValueError(f"workspace {workspace!r}")
         n = get_rmsnorm_backward_workspace_size(rows, K)
         workspace = torch.empty(n, dtype=torch.uint8, device=h.device) if n else None
     if dx is None:
         dx = torch.empty_like(h)
     if dw is None:
         dw = torch.empty(K, dtype=torch.float32, device=h.device)
-    _call("dg_rmsnorm_backward", _raw(dy, None, shape, "dy"), _type_of(dy, "dy"), _raw(h, None, shape, "h"),
-          _type_of(h, "h"), _raw(weight, None, (K,), "weight"), _type_of(weight, "weight"), eps,
-          _raw(dres, h.dtype, shape, "dres"), _raw(dx, h.dtype, shape, "dx"), _raw(dw, torch.float32, (K,), "dw"),
-          rows, K, None if workspace is None else _raw(workspace, torch.uint8, workspace.shape, "workspace"),
-          0 if workspace is None else workspace.numel(), _queue(h))
+    bits = _F32 if h_type else _BF16
+    p = _pointers(index, _NORM_BWD_NAMES, dy, _REAL, shape, h, bits, shape, weight, _REAL, (K,), dres, bits, shape,
+                  dx, bits, shape, dw, _F32, (K,))
+    _call("dg_rmsnorm_backward", p[0], _type_of(dy, "dy"), p[1], h_type, p[2], _type_of(weight, "weight"), eps, p[3],
+          p[4], p[5], rows, K, *_workspace(workspace, index), _raw_stream(index))
     return dx, dw
+
+
+def _workspace(t, index):
+    """Address and bytes of a workspace argument."""
+    if t is None:
+        return None, 0
+    if t.get_device() != index:
+        raise ValueError(f"workspace: on device {t.get_device()}, other arguments on device {index}")
+    return _raw(t, torch.uint8, t.shape, "workspace"), t.numel()
 
 
 def get_gated_workspace_size(M: int, I: int, K: int) -> int:
@@ -587,33 +640,38 @@ def get_gated_workspace_size(M: int, I: int, K: int) -> int:
     return int(v)
 
 
+_GATED_NAMES = ("a", "sfa", "b", "sfb", "gu", "h", "q", "sf")
+
+
 def _gated_args(a, sfa, b, sfb, act, h, q, sf, gu, lead, G, rows, ld):
     """Arguments that the three layouts of the gated GEMM share, and the outputs: lead = leading dimensions of the
     row tensors, G = leading dimensions of b."""
-    I, K = b.shape[-2], b.shape[-1]
+    index = _device(a, "a")
+    I, K = b.shape[-2:]
     packed = sfa.dtype is torch.int32
-    scales = "ue8m0_packed" if packed else "fp32"
-    sf_t = torch.int32 if packed else torch.float32
-    n, blocks = _sf_rows(scales, K // 128), (I + 127) // 128
+    sf_bits = _I32 if packed else _F32
+    n, blocks = _sf_rows(packed, K // 128), (I + 127) // 128
     if h is None and q is None and sf is None:
         h = True
     partial = len(G) > 0                       # rows without data keep what the buffers hold
-    dev = a.device
-    h = _out(h, (*lead, rows, I), torch.bfloat16, dev, partial)
-    gu = _out(gu, (*lead, rows, 2 * I), torch.bfloat16, dev, partial)
-    q = _out(q, (*lead, rows, I), torch.uint8, dev, partial)
-    shape_sf = (*lead, _sf_rows(scales, blocks), ld)
-    if q is not None and (sf is None or sf is True):
-        sf = torch.zeros(shape_sf, dtype=sf_t, device=dev)
+    shape_h = (*lead, rows, I)
+    shape_gu = (*lead, rows, 2 * I)
+    shape_sf = (*lead, _sf_rows(packed, blocks), ld)
+    if h is True or q is True or gu is True or (q is not None and sf is None) or sf is True:
+        dev = a.device
+        h = _out(h, shape_h, torch.bfloat16, dev, partial)
+        gu = _out(gu, shape_gu, torch.bfloat16, dev, partial)
+        q = _out(q, shape_h, torch.uint8, dev, partial)
+        if q is not None and (sf is None or sf is True):
+            sf = torch.zeros(shape_sf, dtype=torch.int32 if packed else torch.float32, device=dev)
+    if q is None:
+        sf = None
     if gu is not None and gu.dim() == len(lead) + 3:
-        gu_shape = (*lead, rows, 2, I)
-    else:
-        gu_shape = (*lead, rows, 2 * I)
-    ins = (_raw(a, _FP8, (*lead, rows, K), "a"), _raw(sfa, sf_t, (*lead, n, ld), "sfa"),
-           _raw(b, _FP8, (*G, 2, I, K), "b"), _raw(sfb, sf_t, (*G, 2, blocks, n), "sfb"))
-    outs = (_raw(gu, torch.bfloat16, gu_shape, "gu"), _raw(h, torch.bfloat16, (*lead, rows, I), "h"),
-            _raw(q, _FP8, (*lead, rows, I), "q"), None if q is None else _raw(sf, sf_t, shape_sf, "sf"))
-    return ins, _act_of(act), outs, (h, q, sf if q is not None else None, gu), I, K, _SUFFIX[scales]
+        shape_gu = (*lead, rows, 2, I)
+    p = _pointers(index, _GATED_NAMES, a, _E4M3, (*lead, rows, K), sfa, sf_bits, (*lead, n, ld), b, _E4M3, (*G, 2, I, K),
+                  sfb, sf_bits, (*G, 2, blocks, n), gu, _BF16, shape_gu, h, _BF16, shape_h, q, _E4M3, shape_h,
+                  sf, sf_bits, shape_sf)
+    return p, _act_of(act), (h, q, sf, gu), I, K, "_ue8m0_packed" if packed else "", index
 
 
 def fp8_gated_gemm_nt(a, sfa, b, sfb, act="silu", h=None, q=None, sf=None, gu=None, workspace="auto"):
@@ -621,21 +679,20 @@ def fp8_gated_gemm_nt(a, sfa, b, sfb, act="silu", h=None, q=None, sf=None, gu=No
     sfb[2, ceil(I/128), K/128]; int32 sfa and sfb are packed power-of-two scales (dg_fp8_gated_gemm_nt_ue8m0_packed).
     act "silu" or "gelu" (tanh form).  Outputs: a tensor to fill, or True for a new one: h[M, I] bf16 (the default),
     q[M, I] E4M3 with sf[I/128 (packed: ceil(I/512)), ld], gu[M, 2I] bf16 (gate, up).  workspace (used for q at small M): a
-    uint8 device tensor of get_gated_workspace_size(M, I, K) bytes, None for none, or "auto".  Returns (h, q, sf, gu), None where not asked for."""
+    uint8 device tensor of get_gated_workspace_size(M, I, K) bytes, None for none, or "auto".  Returns (h, q, sf, gu),
+    None where not asked for."""
     if a.dim() != 2 or b.dim() != 3 or sfa.dim() != 2:
         raise ValueError("a[M, K], sfa[K/128, ld], b[2, I, K]")
     M = a.shape[0]
     ld = sfa.shape[1]
-    ins, act_id, outs, ret, I, K, suffix = _gated_args(a, sfa, b, sfb, act, h, q, sf, gu, (), (), M, ld)
-    stream = _queue(a)
+    p, act_id, ret, I, K, suffix, index = _gated_args(a, sfa, b, sfb, act, h, q, sf, gu, (), (), M, ld)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError(f"workspace {workspace!r}")
         n = get_gated_workspace_size(M, I, K) if ret[1] is not None else 0
         workspace = torch.empty(n, dtype=torch.uint8, device=a.device) if n else None
-    _call("dg_fp8_gated_gemm_nt" + suffix, ins[0], ins[1], ld, ins[2], ins[3], act_id, *outs, ld, M, I, K,
-          None if workspace is None else _raw(workspace, torch.uint8, workspace.shape, "workspace"),
-          0 if workspace is None else workspace.numel(), stream)
+    _call("dg_fp8_gated_gemm_nt" + suffix, p[0], p[1], ld, p[2], p[3], act_id, p[4], p[5], p[6], p[7], ld, M, I, K,
+          *_workspace(workspace, index), _raw_stream(index))
     return ret
 
 
@@ -646,9 +703,10 @@ def m_grouped_fp8_gated_gemm_nt_contiguous(a, sfa, b, sfb, m_indices, act="silu"
     if a.dim() != 2 or b.dim() != 4:
         raise ValueError("a[M_total, K], b[G, 2, I, K]")
     M, G = a.shape[0], b.shape[0]
-    ins, act_id, outs, ret, I, K, suffix = _gated_args(a, sfa, b, sfb, act, h, q, sf, gu, (), (G,), M, M)
-    _call("dg_m_grouped_fp8_gated_gemm_nt_contiguous" + suffix, *ins, act_id, *outs,
-          _raw(m_indices, torch.int32, (M,), "m_indices"), M, I, K, G, _queue(a))
+    p, act_id, ret, I, K, suffix, index = _gated_args(a, sfa, b, sfb, act, h, q, sf, gu, (), (G,), M, M)
+    idx = _pointers(index, ("m_indices",), m_indices, _I32, (M,))
+    _call("dg_m_grouped_fp8_gated_gemm_nt_contiguous" + suffix, p[0], p[1], p[2], p[3], act_id, p[4], p[5], p[6], p[7],
+          idx[0], M, I, K, G, _raw_stream(index))
     return ret
 
 
@@ -659,47 +717,55 @@ def m_grouped_fp8_gated_gemm_nt_masked(a, sfa, b, sfb, masked_m, expected_m=0, a
     data."""
     if a.dim() != 3 or b.dim() != 4:
         raise ValueError("a[G, M_cap, K], b[G, 2, I, K]")
-    G, M = a.shape[0], a.shape[1]
+    G, M = a.shape[:2]
     ld = (M + 3) // 4 * 4
-    ins, act_id, outs, ret, I, K, suffix = _gated_args(a, sfa, b, sfb, act, h, q, sf, gu, (G,), (G,), M, ld)
-    _call("dg_m_grouped_fp8_gated_gemm_nt_masked" + suffix, *ins, act_id, *outs,
-          _raw(masked_m, torch.int32, (G,), "masked_m"), G, M, I, K, int(expected_m), _queue(a))
+    p, act_id, ret, I, K, suffix, index = _gated_args(a, sfa, b, sfb, act, h, q, sf, gu, (G,), (G,), M, ld)
+    counts = _pointers(index, ("masked_m",), masked_m, _I32, (G,))
+    _call("dg_m_grouped_fp8_gated_gemm_nt_masked" + suffix, p[0], p[1], p[2], p[3], act_id, p[4], p[5], p[6], p[7],
+          counts[0], G, M, I, K, int(expected_m), _raw_stream(index))
     return ret
+
+
+_GATED_BWD_NAMES = ("gu", "dh", "m_indices", "dgu", "q", "sf", "qt", "sft", "ht", "sfht")
 
 
 def gated_backward_quantize_e4m3(gu, dh, act="silu", m_indices=None, dgu=None, q=None, sf=None, qt=None, sft=None,
                                  ht=None, sfht=None, ue8m0=False):
     """Gradient of h = act(gate) * up, quantised (dg_gated_backward_quantize_e4m3[_ue8m0]): gu[rows, 2I] and
-    dh[rows, I] bf16, m_indices[rows] int32 or None (rows with a negative index count as zeros).  Outputs, each a tensor to fill or
-    True for a new one (scales are allocated with their codes): dgu[rows, 2I] bf16; q[rows, 2I] with sf[2I/128, ld];
-    qt[R, 2I] with sft[R/128, 2I] and ht[R, I] with sfht[R/128, I], R = rows up to a multiple of 128.
+    dh[rows, I] bf16, m_indices[rows] int32 or None (rows with a negative index count as zeros).  Outputs, each a
+    tensor to fill or True for a new one (scales are allocated with their codes): dgu[rows, 2I] bf16; q[rows, 2I] with
+    sf[2I/128, ld]; qt[R, 2I] with sft[R/128, 2I] and ht[R, I] with sfht[R/128, I], R = rows up to a multiple of 128.
     Returns (dgu, q, sf, qt, sft, ht, sfht), None where not asked for."""
     if dh.dim() != 2:
         raise ValueError("dh[rows, I]")
     rows, I = dh.shape
+    index = _device(dh, "dh")
     full = (rows + 127) // 128
-    dev = dh.device
+    wide, wide_full, slim_full = (rows, 2 * I), (full * 128, 2 * I), (full * 128, I)
     f32 = torch.float32
-    dgu = _out(dgu, (rows, 2 * I), torch.bfloat16, dev)
-    q, qt, ht = (_out(q, (rows, 2 * I), torch.uint8, dev), _out(qt, (full * 128, 2 * I), torch.uint8, dev),
-                 _out(ht, (full * 128, I), torch.uint8, dev))
-    if q is not None and sf is None:
-        sf = torch.zeros((2 * I // 128, (rows + 3) // 4 * 4), dtype=f32, device=dev)
-    if qt is not None and sft is None:
-        sft = torch.empty((full, 2 * I), dtype=f32, device=dev)
-    if ht is not None and sfht is None:
-        sfht = torch.empty((full, I), dtype=f32, device=dev)
-    ld = sf.shape[-1] if q is not None else 0
-    bf16 = torch.bfloat16
-    _call("dg_gated_backward_quantize_e4m3" + ("_ue8m0" if ue8m0 else ""),
-          _raw(gu, bf16, (rows, 2, I) if gu.dim() == 3 else (rows, 2 * I), "gu"), _raw(dh, bf16, (rows, I), "dh"),
-          _act_of(act), _raw(m_indices, torch.int32, (rows,), "m_indices"), _raw(dgu, bf16, (rows, 2 * I), "dgu"),
-          _raw(q, _FP8, (rows, 2 * I), "q"), None if q is None else _raw(sf, f32, (2 * I // 128, ld), "sf"), ld,
-          _raw(qt, _FP8, (full * 128, 2 * I), "qt"), None if qt is None else _raw(sft, f32, (full, 2 * I), "sft"),
-          _raw(ht, _FP8, (full * 128, I), "ht"), None if ht is None else _raw(sfht, f32, (full, I), "sfht"),
-          rows, I, _queue(dh))
-    return (dgu, q, sf if q is not None else None, qt, sft if qt is not None else None, ht,
-            sfht if ht is not None else None)
+    if True in (dgu is True, q is True, qt is True, ht is True):
+        dev = dh.device
+        dgu = _out(dgu, wide, torch.bfloat16, dev)
+        q, qt, ht = _out(q, wide, torch.uint8, dev), _out(qt, wide_full, torch.uint8, dev), _out(ht, slim_full, torch.uint8, dev)
+    if q is None:
+        sf = None
+    elif sf is None:
+        sf = torch.zeros((2 * I // 128, (rows + 3) // 4 * 4), dtype=f32, device=dh.device)
+    if qt is None:
+        sft = None
+    elif sft is None:
+        sft = torch.empty((full, 2 * I), dtype=f32, device=dh.device)
+    if ht is None:
+        sfht = None
+    elif sfht is None:
+        sfht = torch.empty((full, I), dtype=f32, device=dh.device)
+    ld = sf.shape[-1] if sf is not None else 0
+    p = _pointers(index, _GATED_BWD_NAMES, gu, _BF16, (rows, 2, I) if gu.dim() == 3 else wide, dh, _BF16, (rows, I),
+                  m_indices, _I32, (rows,), dgu, _BF16, wide, q, _E4M3, wide, sf, _F32, (2 * I // 128, ld),
+                  qt, _E4M3, wide_full, sft, _F32, (full, 2 * I), ht, _E4M3, slim_full, sfht, _F32, (full, I))
+    _call("dg_gated_backward_quantize_e4m3" + ("_ue8m0" if ue8m0 else ""), p[0], p[1], _act_of(act), p[2], p[3], p[4],
+          p[5], ld, p[6], p[7], p[8], p[9], rows, I, _raw_stream(index))
+    return dgu, q, sf, qt, sft, ht, sfht
 
 
 def get_mk_alignment_for_contiguous_layout() -> int:

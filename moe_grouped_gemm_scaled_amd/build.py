@@ -3,7 +3,8 @@
     python -m moe_grouped_gemm_scaled_amd.build
 
 Every source is compiled ahead of time (no JIT); the object files go to
-_build/ next to this file and the shared library to libdg.so beside it.
+_build/ next to this file and the shared library to libdg.so beside it, with
+_args.so, the native argument checks of the Python binding.
 """
 import os
 import subprocess
@@ -14,6 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdg.so")
+ARGS = os.path.join(HERE, "_args.so")     # the binding's argument checks, a Python extension module
 SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "decode.hip", "pipelined.hip", "persistent.hip", "mqa.hip", "noalloc.hip", "stream.hip",
            "layer_api.cpp", "norm.hip", "gated.hip", "gated_small.hip", "gated_bwd.hip"]
 ARCH = "gfx950"
@@ -28,6 +30,21 @@ def _hipcc():
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     path = os.path.join(rocm, "bin", "hipcc")
     return path if os.path.exists(path) else "hipcc"
+
+
+def _args_command():
+    """Compiles the binding's argument checks (csrc/py_args.cpp, host code against torch's headers)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+            + [a for i in inc for a in ("-isystem", i)]
+            + [os.path.join(CSRC, "py_args.cpp"), "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+               "-Wl,-rpath," + lib, "-o", ARGS + ".tmp"])
 
 
 def build(verbose: bool = False) -> str:
@@ -47,6 +64,7 @@ def build(verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    procs.append(("py_args.cpp", subprocess.Popen(_args_command(), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -65,6 +83,7 @@ def build(verbose: bool = False) -> str:
     cmd = [hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}"] + objs + ["-o", tmp]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    os.replace(ARGS + ".tmp", ARGS)
     if verbose:
         print(f"built {LIB} in {time.time() - t0:.1f}s", file=sys.stderr)
     return LIB
