@@ -521,8 +521,9 @@ int64_t dg_get_rmsnorm_backward_workspace_size(int rows, int K);
  * [ceil(K/512)][ld_sfa], sfb [2][ceil(I/128)][ceil(K/512)]) and writes such
  * scales (sf [ceil(I/512)][ld_sf]), as dg_fp8_gemm_nt_ue8m0_packed takes them.
  *   workspace: dg_get_gated_workspace_size(M, I, K) bytes of device memory,
- *   16-byte aligned, of any content, for a q output at small M (0 bytes
- *   elsewhere); calls that may run at the same time need one each.  With NULL,
+ *   16-byte aligned, of any content, for a q output of problems too small to
+ *   fill the CUs with 128-column tiles (0 bytes elsewhere); calls that may run
+ *   at the same time need one each.  With NULL,
  *   or too few bytes, a kernel that needs none (and is slower there) computes
  *   the same outputs.
  * Errors: DG_ERR_NULL; DG_ERR_SHAPE (M < 0; I < 1; K < 128 or K % 128; q with

@@ -678,7 +678,7 @@ def fp8_gated_gemm_nt(a, sfa, b, sfb, act="silu", h=None, q=None, sf=None, gu=No
     """h = act(A Wg^T) * (A Wu^T) in one kernel (dg_fp8_gated_gemm_nt): a[M, K], sfa[K/128, ld], b[2, I, K] (Wg, Wu),
     sfb[2, ceil(I/128), K/128]; int32 sfa and sfb are packed power-of-two scales (dg_fp8_gated_gemm_nt_ue8m0_packed).
     act "silu" or "gelu" (tanh form).  Outputs: a tensor to fill, or True for a new one: h[M, I] bf16 (the default),
-    q[M, I] E4M3 with sf[I/128 (packed: ceil(I/512)), ld], gu[M, 2I] bf16 (gate, up).  workspace (used for q at small M): a
+    q[M, I] E4M3 with sf[I/128 (packed: ceil(I/512)), ld], gu[M, 2I] bf16 (gate, up).  workspace (used for q of small problems): a
     uint8 device tensor of get_gated_workspace_size(M, I, K) bytes, None for none, or "auto".  Returns (h, q, sf, gu),
     None where not asked for."""
     if a.dim() != 2 or b.dim() != 3 or sfa.dim() != 2:

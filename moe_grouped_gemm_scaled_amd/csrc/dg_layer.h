@@ -76,6 +76,7 @@ hipError_t launch_gated(const GatedProblem &p, int num_cus, hipStream_t stream, 
 
 // Its kernel for few rows (dense): takes the problem or not (a quantised
 // output needs scratch of gated_small_workspace bytes).
+constexpr int kGatedSmallMaxM = 128;
 bool gated_small_takes(const GatedProblem &p, int num_cus);
 size_t gated_small_workspace(int M, int I, int K, int num_cus);
 hipError_t launch_gated_small(const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config);

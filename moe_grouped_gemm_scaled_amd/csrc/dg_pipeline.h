@@ -148,36 +148,52 @@ __device__ __forceinline__ int contig_unit_block(const int32_t *idx, int nblocks
     return -1;
 }
 
-// The same walk to its end: returns the first block of unit u (-1 for none, or
-// u < 0) and leaves the number of units in `units`.
-__device__ __forceinline__ int contig_scan(const int32_t *idx, int nblocks, int u, int &units) {
-    const int lane = threadIdx.x & 63;
-    int prev_e = -1;     // expert of the block before this round (none: -1)
-    int seg = -1;        // first block of the segment running into this round
-    int count = 0, found = -1;
-    for (int base = 0; base < nblocks; base += 64) {
-        const int b = base + lane;
-        const int e = b < nblocks ? idx[(int64_t)b * 128] : -1;
-        int ep = __shfl_up(e, 1);
-        if (lane == 0) ep = prev_e;
-        int sg = e >= 0 && e != ep ? b : -1;      // inclusive max-scan of segment starts
+// Expert indices of blocks base + 64 q + lane (-1 past the end): one round of
+// contig_scan, all loads in flight together.
+struct ContigBlocks {
+    int e[4];
+};
+__device__ __forceinline__ ContigBlocks contig_load(const int32_t *idx, int nblocks, int base) {
+    ContigBlocks r;
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int t = __shfl_up(sg, o);
-            if (lane >= o) sg = sg > t ? sg : t;
+    for (int q = 0; q < 4; ++q) {
+        const int b = base + 64 * q + (int)(threadIdx.x & 63);
+        r.e[q] = b < nblocks ? idx[(int64_t)b * 128] : -1;
+    }
+    return r;
+}
+
+// The walk of contig_unit_block to its end: returns the first block of unit u
+// (-1 for none, or u < 0) and leaves the number of units in `units`.  `first`:
+// the first round's blocks, which two walks can share.
+__device__ __forceinline__ int contig_scan(const int32_t *idx, int nblocks, const ContigBlocks &first, int u, int &units) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t upto = ~0ull >> (63 - lane);   // this lane and those before it
+    int prev_e = -1;     // expert of the block before this step (none: -1)
+    int seg = -1;        // first block of the segment running into this step
+    int count = 0, found = -1;
+    for (int base = 0; base < nblocks; base += 256) {
+        ContigBlocks r = first;
+        if (base > 0) r = contig_load(idx, nblocks, base);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int e = r.e[q], b0 = base + 64 * q;
+            int ep = __shfl_up(e, 1);
+            if (lane == 0) ep = prev_e;
+            const uint64_t starts = __ballot(e >= 0 && e != ep);
+            const int sg = starts & upto ? b0 + 63 - __clzll((long long)(starts & upto)) : seg;
+            const bool unit = e >= 0 && ((b0 + lane - sg) & 1) == 0;
+            const uint64_t m = __ballot(unit);
+            const int n = __popcll(m);
+            if (u >= count && u < count + n) {
+                const int rank = __popcll(m & (upto >> 1));
+                const uint64_t hit = __ballot(unit && rank == u - count);
+                found = b0 + __ffsll((unsigned long long)hit) - 1;
+            }
+            count += n;
+            prev_e = __shfl(e, 63);
+            seg = __shfl(sg, 63);
         }
-        sg = sg > seg ? sg : seg;
-        const bool unit = e >= 0 && ((b - sg) & 1) == 0;
-        const uint64_t m = __ballot(unit);
-        const int n = __popcll(m);
-        if (u >= count && u < count + n) {
-            const int rank = __popcll(m & ((1ull << lane) - 1ull));
-            const uint64_t hit = __ballot(unit && rank == u - count);
-            found = base + __ffsll((unsigned long long)hit) - 1;
-        }
-        count += n;
-        prev_e = __shfl(e, 63);
-        seg = __shfl(sg, 63);
     }
     units = count;
     return found;

@@ -78,4 +78,19 @@ __device__ __forceinline__ uint32_t encode4(const v4f &v, const BlockDivisor &d)
     return e4m3_encode4(divide<UE8M0>(v.x, d), divide<UE8M0>(v.y, d), divide<UE8M0>(v.z, d), divide<UE8M0>(v.w, d));
 }
 
+// Scale of block nb (of nnb) of a row, in K-block-major scales of ld columns:
+// fp32, or packed (PK): byte nb % 4 of the row's word, where the last block
+// clears the bytes past it.
+template <bool PK>
+__device__ __forceinline__ void store_block_scale(uint32_t *sf, int ld, int64_t row, int nb, int nnb, float s) {
+    if constexpr (PK) {
+        uint8_t *w = reinterpret_cast<uint8_t *>(sf + (int64_t)(nb / 4) * ld + row);
+        w[nb & 3] = (uint8_t)(__float_as_uint(s) >> 23);
+        if (nb == nnb - 1)
+            for (int e = (nb & 3) + 1; e < 4; ++e) w[e] = 0;
+    } else {
+        sf[(int64_t)nb * ld + row] = __float_as_uint(s);
+    }
+}
+
 }  // namespace dg

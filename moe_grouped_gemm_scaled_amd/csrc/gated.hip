@@ -12,13 +12,16 @@
 //
 // Organisation: the LDS-DMA pipeline of the plain GEMM (constant-count waits,
 // XOR-swizzled stages, see pipelined.hip), with a column tile that holds the
-// same 128 columns of both projections: of the 64 B rows that a wave
-// multiplies, 32 are gate rows and 32 the up rows of the same columns, so a
-// lane ends up with both factors of its h values in its own registers and the
-// product needs no exchange.  128 columns are also one quantisation block of
-// the next GEMM's K axis: a row's scale is a maximum over the tile's row,
-// four values per row through LDS.  Outputs are staged in LDS as whole rows,
-// so that every store instruction writes whole lines.
+// same columns of both projections: of the B rows that a wave multiplies, half
+// are gate rows and half the up rows of the same columns, so a lane ends up
+// with both factors of its h values in its own registers and the product needs
+// no exchange.  128 columns are also one quantisation block of the next GEMM's
+// K axis: a row's scale is a maximum over the tile's row, four values per row
+// through LDS.  Narrower tiles, which fill the CUs where 128 columns would
+// leave most of them idle, hold no whole block: they leave h in fp32 in the
+// caller's workspace, and a second kernel encodes it (4 us, 901 rows, I = 512).
+// Outputs are staged in LDS as whole rows, so that every store instruction
+// writes whole lines.
 #include <stdio.h>
 
 #include "dg_act.h"
@@ -26,6 +29,7 @@
 #include "dg_layer.h"
 #include "dg_pipeline.h"
 #include "dg_quant.h"
+#include "dg_rows.h"
 
 namespace dg {
 
@@ -42,6 +46,7 @@ struct GatedArgs {
     int tiles_m, tiles_n, gm;
     int part, cus;             // contiguous: which rows this launch takes (ContigPart)
     int sa_cols;               // columns of sfa from the first row on (ld_sfa, less the rows before it)
+    float *hq;                 // tiles of fewer than 128 columns: h of a quantised output in fp32, [rows][I]
 };
 
 // The contiguous layout can take two launches: 256-row units that fill the CUs
@@ -66,11 +71,11 @@ __device__ __forceinline__ int staged(int r, int c) {
     return (r * CPR + (c ^ (r & (CPR - 1)))) * 16;
 }
 
-template <int BM, int WGM, int WGN, int NST, Mode MODE, bool PK>
-__global__ void __launch_bounds__(64 * WGM * WGN)
+template <int BM, int BH, int NST, Mode MODE, bool PK>
+__global__ void __launch_bounds__(512, BH == 32 ? 4 : 2)   // waves per SIMD: two workgroups of the smallest tile share a CU
 gated_kernel(GatedArgs p) {
-    constexpr int BN = 256, BH = 128;             // B rows of a tile, columns of h
-    constexpr int NW = WGM * WGN;
+    constexpr int BN = 2 * BH;                    // B rows of a tile
+    constexpr int NW = 8, WGN = BN >= 128 ? 4 : BN / 32, WGM = NW / WGN;   // waves
     constexpr int TM = BM / WGM, TN = BN / WGN;   // wave tile
     constexpr int TH = TN / 2;                    // columns of h per wave
     constexpr int SM = TM / 16, SN = TN / 16;     // MFMA subtiles per wave
@@ -83,20 +88,22 @@ gated_kernel(GatedArgs p) {
     constexpr int STAGE = OFF_JUNK + 1024;
     constexpr int DA = BM / (8 * NW), DB = BN / (8 * NW);   // 1-KB LDS-DMA chunks per wave per K block
     constexpr int PER_BLOCK = DA + DB + 1;
-    static_assert(NST >= 2 && NST <= 3 && NST * STAGE + BM * (WGN * 4 + 1) <= 160 * 1024, "LDS");
+    static_assert(NST >= 2 && NST <= 4 && NST * STAGE + BM * (WGN * 4 + 1) <= 160 * 1024, "LDS");
     static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM / 4 <= 64 && NW >= 2, "DMA chunks");
     static_assert((NST - 2) * PER_BLOCK < 64, "vmcnt immediate");
-    static_assert(TH % 16 == 0 && BM * 256 <= STAGE, "a staged output tile fits one stage");
+    static_assert(TH % 16 == 0 && BM * BH * 2 <= STAGE, "a staged output tile fits one stage");
 
     __shared__ __attribute__((aligned(16))) uint8_t stage0[STAGE];
     __shared__ __attribute__((aligned(16))) uint8_t stage1[STAGE];
     __shared__ __attribute__((aligned(16))) uint8_t stage2[NST > 2 ? STAGE : 16];
-    __shared__ float row_max[WGN][BM];
+    __shared__ __attribute__((aligned(16))) uint8_t stage3[NST > 3 ? STAGE : 16];
+    __shared__ float row_max[WGN][BH == 128 ? BM : 1];
     auto stage_of = [&](auto sc) __attribute__((always_inline)) -> uint8_t * {
         constexpr int s = decltype(sc)::value;
         if constexpr (s == 0) return stage0;
         else if constexpr (s == 1) return stage1;
-        else return stage2;
+        else if constexpr (s == 2) return stage2;
+        else return stage3;
     };
 
     const int K = p.K, I = p.I;
@@ -106,18 +113,20 @@ gated_kernel(GatedArgs p) {
     const int tiles_per_group = p.tiles_m * p.tiles_n;
     // contiguous: the first row block and the number of row tiles of this launch
     int tiles_m = p.tiles_m, block0 = 0;
+    ContigBlocks blocks;
+    const int nblocks = p.rows_a / 128;
     if constexpr (MODE == Mode::Contig) {
-        const int nblocks = p.rows_a / 128;
+        if (BM == 256 || p.part != kAllRows) blocks = contig_load(p.idx, nblocks, 0);
         if (p.part != kAllRows) {
             int units = 0;
-            contig_scan(p.idx, nblocks, -1, units);
+            contig_scan(p.idx, nblocks, blocks, -1, units);
             const int head = head_units(units, p.tiles_n, p.cus);
             if (BM == 256) {
                 tiles_m = head;
             } else {
                 if (head >= units) return;         // no tail: uniform exit
                 int u = 0;
-                block0 = head > 0 ? contig_scan(p.idx, nblocks, head, u) : 0;
+                block0 = head > 0 ? contig_scan(p.idx, nblocks, blocks, head, u) : 0;
                 tiles_m = (nblocks - block0) * 128 / BM;
             }
         }
@@ -137,7 +146,7 @@ gated_kernel(GatedArgs p) {
     int m0 = block0 * 128 + tm * BM;
     if constexpr (MODE == Mode::Contig && BM == 256) {
         int units = 0;
-        const int ub = __builtin_amdgcn_readfirstlane(contig_scan(p.idx, p.rows_a / 128, tm, units));
+        const int ub = __builtin_amdgcn_readfirstlane(contig_scan(p.idx, nblocks, blocks, tm, units));
         if (ub < 0) return;                        // no such unit: uniform exit
         m0 = ub * 128;
     }
@@ -344,14 +353,15 @@ gated_kernel(GatedArgs p) {
         return r < rows && (MODE != Mode::Contig || of_expert[r]);
     };
     const int64_t row0 = row_base + m0;
-    // staged bf16 tile (256-byte rows) to columns n0 .. n0+127 of out [..][pitch]
+    // staged bf16 tile to columns n0 .. n0+BH-1 of out [..][pitch]
+    constexpr int CPR = BH / 8;                    // 16-byte chunks per row
     auto store_bf16 = [&](const uint8_t *stg, uint16_t *out, int64_t pitch) __attribute__((always_inline)) {
         const bool vec = (I % 8) == 0;
-        for (int item = tid; item < BM * 16; item += 64 * NW) {
-            const int r = item >> 4, c = item & 15;
+        for (int item = tid; item < BM * CPR; item += 64 * NW) {
+            const int r = item / CPR, c = item % CPR;
             const int col = n0 + 8 * c;
             if (!row_ok(r) || col >= I) continue;
-            const v4i v = *reinterpret_cast<const v4i *>(stg + staged<16>(r, c));
+            const v4i v = *reinterpret_cast<const v4i *>(stg + staged<CPR>(r, c));
             uint16_t *o = out + (row0 + r) * pitch + col;
             if (vec) {
                 __builtin_nontemporal_store(v, reinterpret_cast<v4i *>(o));
@@ -366,7 +376,7 @@ gated_kernel(GatedArgs p) {
     auto stage_bf16 = [&](uint8_t *stg, int i, int j, const v4f &v) __attribute__((always_inline)) {
         const int r = wm * TM + 16 * i + l16;
         const int c = (wn * TH + 16 * j) / 8 + (g4 >> 1);
-        *reinterpret_cast<uint2 *>(stg + staged<16>(r, c) + 8 * (g4 & 1)) =
+        *reinterpret_cast<uint2 *>(stg + staged<CPR>(r, c) + 8 * (g4 & 1)) =
             uint2{pack_bf16x2_rne(v.x, v.y), pack_bf16x2_rne(v.z, v.w)};
     };
     if (p.gu) {                                    // uniform
@@ -412,7 +422,19 @@ gated_kernel(GatedArgs p) {
         lds_barrier();
         store_bf16(stage0, p.h, I);
     }
-    if (p.q) {                                     // uniform; I is a multiple of 128
+    if constexpr (BH < 128) {                      // no whole quantisation block: gated_encode_kernel takes over
+        if (p.hq) {                                // uniform; I is a multiple of 128
+            static_for<SM>([&](auto ic) __attribute__((always_inline)) {
+                constexpr int i = decltype(ic)::value;
+                const int r = wm * TM + 16 * i + l16;
+                static_for<SH>([&](auto jc) __attribute__((always_inline)) {
+                    constexpr int j = decltype(jc)::value;
+                    if (r < rows)
+                        *reinterpret_cast<v4f *>(p.hq + (row0 + r) * I + n0 + wn * TH + 16 * j + 4 * g4) = acc[i][j];
+                });
+            });
+        }
+    } else if (p.q) {                              // uniform; I is a multiple of 128
         // the row's maximum over this wave's TH columns, then over the waves
         static_for<SM>([&](auto ic) __attribute__((always_inline)) {
             constexpr int i = decltype(ic)::value;
@@ -439,18 +461,8 @@ gated_kernel(GatedArgs p) {
                 *reinterpret_cast<uint32_t *>(stage1 + staged<8>(r, wn * SH + j) + 4 * g4) =
                     encode4<PK>(acc[i][j], d);
             });
-            if (wn == 0 && g4 == 0 && row_ok(r)) {
-                const int nb = n0 / 128;
-                if constexpr (PK) {
-                    // byte nb % 4 of the row's word; the last block clears the bytes past it
-                    uint8_t *w = static_cast<uint8_t *>(p.sf) + (sf_base + (int64_t)(nb / 4) * p.ld_sf + m0 + r) * 4;
-                    w[nb & 3] = (uint8_t)(__float_as_uint(s) >> 23);
-                    if (nb == nnb - 1)
-                        for (int e = (nb & 3) + 1; e < 4; ++e) w[e] = 0;
-                } else {
-                    static_cast<float *>(p.sf)[sf_base + (int64_t)nb * p.ld_sf + m0 + r] = s;
-                }
-            }
+            if (wn == 0 && g4 == 0 && row_ok(r))
+                store_block_scale<PK>(static_cast<uint32_t *>(p.sf) + sf_base, p.ld_sf, m0 + r, n0 / 128, nnb, s);
         });
         lds_barrier();
         for (int item = tid; item < BM * 8; item += 64 * NW) {
@@ -462,15 +474,37 @@ gated_kernel(GatedArgs p) {
     }
 }
 
-template <int BM, int NST, Mode MODE, bool PK>
+// E4M3 blocks of h from fp32: 16 lanes per (row, 128-column block).
+template <bool PK>
+__global__ void __launch_bounds__(256) gated_encode_kernel(GatedArgs p) {
+    const int lane16 = threadIdx.x & 15;
+    const int I = p.I, nnb = I / 128;
+    const int64_t unit = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int nb = (int)(unit % nnb);
+    const int64_t row = unit / nnb;
+    if (row >= p.rows_a) return;                   // whole groups of 16 lanes
+    const int64_t o = row * I + 128 * nb + 8 * lane16;
+    const Raw8<float> v = load8(p.hq + o);
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(get8(v, e)));
+    const float s = block_scale<PK>(max16(m));
+    const BlockDivisor d = block_divisor<PK>(s);
+    *reinterpret_cast<uint2 *>(p.q + o) =
+        uint2{encode4<PK>(v4f{get8(v, 0), get8(v, 1), get8(v, 2), get8(v, 3)}, d),
+              encode4<PK>(v4f{get8(v, 4), get8(v, 5), get8(v, 6), get8(v, 7)}, d)};
+    if (lane16 == 0) store_block_scale<PK>(static_cast<uint32_t *>(p.sf), p.ld_sf, row, nb, nnb, s);
+}
+
+template <int BM, int BH, int NST, Mode MODE, bool PK>
 static hipError_t launch_t(const GatedProblem &p, int num_cus, ContigPart part, hipStream_t stream,
                            std::string &config) {
     GatedArgs k{p.a, p.sfa, p.b, p.sfb, p.idx, p.gu, p.h, p.q, p.sf, p.rows_a, p.I, p.K, p.ld_sfa, p.ld_sf, p.G, p.act,
-                0, 0, 4, part, num_cus, p.ld_sfa - p.row0};
+                0, 0, 4, part, num_cus, p.ld_sfa - p.row0, BH < 128 && p.q ? static_cast<float *>(p.ws) : nullptr};
     k.tiles_m = (p.rows_a + BM - 1) / BM;
     // contiguous 256-row units: at most one per 256 rows plus one per expert segment
     if (MODE == Mode::Contig && BM == 256) k.tiles_m = p.rows_a / 256 + p.G + 1;
-    k.tiles_n = (p.I + 127) / 128;
+    k.tiles_n = (p.I + BH - 1) / BH;
     int64_t grid = (int64_t)k.tiles_m * k.tiles_n * (MODE == Mode::Masked ? p.G : 1);
     if (part == kTail) {
         // at most half the CUs' worth of 256-row units, two blocks each, and
@@ -480,37 +514,65 @@ static hipError_t launch_t(const GatedProblem &p, int num_cus, ContigPart part, 
     }
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     char buf[160];
-    snprintf(buf, sizeof buf, "%sfamily=gated mode=%d tile=%dx%dx128 waves=2x4 stages=%d grid=%lld%s",
-             config.empty() ? "" : " + ", (int)MODE, BM, 256, NST, (long long)grid, PK ? " scales=ue8m0_packed" : "");
+    snprintf(buf, sizeof buf, "%sfamily=gated mode=%d tile=%dx%dx128 stages=%d grid=%lld%s",
+             config.empty() ? "" : " + ", (int)MODE, BM, 2 * BH, NST, (long long)grid, PK ? " scales=ue8m0_packed" : "");
     config += buf;
-    hipLaunchKernelGGL((gated_kernel<BM, 2, 4, NST, MODE, PK>), dim3((unsigned)grid), dim3(512), 0, stream, k);
+    hipLaunchKernelGGL((gated_kernel<BM, BH, NST, MODE, PK>), dim3((unsigned)grid), dim3(512), 0, stream, k);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess || !k.hq) return err;
+    const int64_t blocks = (int64_t)p.rows_a * (p.I / 128);
+    hipLaunchKernelGGL(gated_encode_kernel<PK>, dim3((unsigned)((blocks + 15) / 16)), dim3(256), 0, stream, k);
     return hipGetLastError();
 }
 
-// Rows of a tile.  A round of tiles over the CUs takes about 100, 60 and 40
-// (measured, K = 7168: 88 to 108, 53 to 60 and 40 us) with 256, 128 and 64 rows:
-// smaller tiles multiply less per byte they load, but fill the CUs where there
-// are few rows.
-static int tile_rows(int rows, int groups, int64_t tiles_n, int num_cus) {
-    int best = 256;
+// Tiles, rows x columns of h, and what a round of them over the CUs costs per K
+// block, in hundredths of a round of 256x128 (measured, I = 2048, K = 7168:
+// 97 to 103 us at 256x128 with packed scales, 57 to 60 at 128x128, 39 to 41 at
+// 128x64, 38 (packed) to 46 (fp32 scales) at 64x128, 26.3 at 64x64 and 18.0 at
+// 64x32).  Small tiles multiply less per byte they load, but fill the CUs: 256
+// rows take 18.0 us in 64x32 tiles, 33 in 64x128 ones.  Three stages: two cost
+// 30 to 40 % more with the narrow tiles, four gain nothing.
+struct Tile {
+    int rows, cols, cost;
+};
+constexpr Tile kTiles[] = {{256, 128, 100}, {128, 128, 60}, {128, 64, 38}, {64, 128, 41}, {64, 64, 25}, {64, 32, 17}};
+// Prologue and epilogue of a round, and the second kernel of a narrow tile with
+// a quantised output, in the same unit (18 ns).
+constexpr int kRoundCost = 150, kEncodeCost = 300;
+
+// narrow: tiles of fewer than 128 columns can serve.  encode: they need the
+// second kernel.  spare: rows that 256-row tiles waste besides.
+static Tile choose_tile(int rows, int spare, int groups, int I, int K, bool narrow, bool encode, int num_cus) {
+    Tile best = kTiles[0];
     int64_t least = INT64_MAX;
-    const int bm[3] = {256, 128, 64}, cost[3] = {100, 60, 40};
-    for (int i = 0; i < 3; ++i) {
-        const int64_t tiles = (int64_t)groups * ((rows + bm[i] - 1) / bm[i]) * tiles_n;
-        const int64_t c = (tiles + num_cus - 1) / num_cus * cost[i];
+    for (const Tile &t : kTiles) {
+        if (t.cols < 128 && !narrow) continue;
+        const int64_t tiles = groups * ((rows + (t.rows == 256 ? (int64_t)spare : 0) + t.rows - 1) / t.rows) * ((I + t.cols - 1) / t.cols);
+        const int64_t c = (tiles + num_cus - 1) / num_cus * ((int64_t)t.cost * (K / kKBlock) + kRoundCost) +
+                          (t.cols < 128 && encode ? kEncodeCost : 0);
         if (c < least) {
             least = c;
-            best = bm[i];
+            best = t;
         }
     }
     return best;
 }
 
 template <Mode MODE, bool PK>
-static hipError_t launch_rows(int rows, const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config) {
-    if (rows == 256) return launch_t<256, 2, MODE, PK>(p, num_cus, kAllRows, stream, config);
-    if (rows == 128) return launch_t<128, 3, MODE, PK>(p, num_cus, kAllRows, stream, config);
-    return launch_t<64, 3, MODE, PK>(p, num_cus, kAllRows, stream, config);
+static hipError_t launch_tile(Tile t, const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config) {
+    if (t.rows == 256) return launch_t<256, 128, 2, MODE, PK>(p, num_cus, kAllRows, stream, config);
+    if (t.rows == 128)
+        return t.cols == 128 ? launch_t<128, 128, 3, MODE, PK>(p, num_cus, kAllRows, stream, config)
+                             : launch_t<128, 64, 3, MODE, PK>(p, num_cus, kAllRows, stream, config);
+    return t.cols == 128  ? launch_t<64, 128, 3, MODE, PK>(p, num_cus, kAllRows, stream, config)
+           : t.cols == 64 ? launch_t<64, 64, 3, MODE, PK>(p, num_cus, kAllRows, stream, config)
+                          : launch_t<64, 32, 3, MODE, PK>(p, num_cus, kAllRows, stream, config);
+}
+
+// Dense: rows of the full rounds of 256x128 tiles.
+static int head_rows(int rows, int I, int num_cus) {
+    const int64_t tiles_n = (I + 127) / 128;
+    return (int)(rows / 256 * tiles_n / num_cus * num_cus / tiles_n * 256);
 }
 
 template <bool PK>
@@ -520,12 +582,11 @@ static hipError_t launch_pk(const GatedProblem &p, int num_cus, hipStream_t stre
     case Mode::Dense: {
         // full rounds of 256-row tiles, then the rows that are left in tiles of
         // their own choice (4500 rows: 16 row tiles of 256, then 64-row tiles)
-        const int64_t row_tiles = p.rows_a / 256, full = row_tiles * tiles_n / num_cus * num_cus / tiles_n;
-        const int head = (int)(full * 256), rest = p.rows_a - head;
+        const int head = head_rows(p.rows_a, p.I, num_cus), rest = p.rows_a - head;
         if (head > 0) {
             GatedProblem q = p;
             q.rows_a = head;
-            const hipError_t err = launch_t<256, 2, Mode::Dense, PK>(q, num_cus, kAllRows, stream, config);
+            const hipError_t err = launch_t<256, 128, 2, Mode::Dense, PK>(q, num_cus, kAllRows, stream, config);
             if (err != hipSuccess || rest == 0) return err;
         }
         GatedProblem q = p;
@@ -539,29 +600,37 @@ static hipError_t launch_pk(const GatedProblem &p, int num_cus, hipStream_t stre
             q.q += (int64_t)head * p.I;
             q.sf = static_cast<uint32_t *>(p.sf) + head;
         }
-        return launch_rows<Mode::Dense, PK>(tile_rows(rest, 1, tiles_n, num_cus), q, num_cus, stream, config);
+        const bool scratch = p.ws && p.ws_bytes >= (size_t)rest * p.I * sizeof(float);
+        const Tile t = choose_tile(rest, 0, 1, p.I, p.K, !p.q || scratch, p.q != nullptr, num_cus);
+        return launch_tile<Mode::Dense, PK>(t, q, num_cus, stream, config);
     }
     case Mode::Contig: {
         // every expert's last unit may hold one block only: one more 256-row tile each
-        const int rows = tile_rows(p.rows_a + 128 * p.G, 1, tiles_n, num_cus);
-        if (rows == 64 || p.rows_a < 256) return launch_rows<Mode::Contig, PK>(rows == 256 ? 128 : rows, p, num_cus, stream, config);
-        if (rows == 128 && p.rows_a / 128 * tiles_n <= num_cus)
-            return launch_rows<Mode::Contig, PK>(128, p, num_cus, stream, config);
-        const hipError_t err = launch_t<256, 2, Mode::Contig, PK>(p, num_cus, kHead, stream, config);
+        const Tile t = choose_tile(p.rows_a, 128 * p.G, 1, p.I, p.K, !p.q, false, num_cus);
+        if (t.rows == 64 || t.cols < 128) return launch_tile<Mode::Contig, PK>(t, p, num_cus, stream, config);
+        if (p.rows_a < 256 || (t.rows == 128 && p.rows_a / 128 * tiles_n <= num_cus))
+            return launch_tile<Mode::Contig, PK>(kTiles[1], p, num_cus, stream, config);
+        const hipError_t err = launch_t<256, 128, 2, Mode::Contig, PK>(p, num_cus, kHead, stream, config);
         if (err != hipSuccess) return err;
-        return launch_t<128, 3, Mode::Contig, PK>(p, num_cus, kTail, stream, config);
+        return launch_t<128, 128, 3, Mode::Contig, PK>(p, num_cus, kTail, stream, config);
     }
     case Mode::Masked: {
         // the groups' counts are on the device: the caller's hint, or the capacity
         const int expect = p.expected_m > 0 && p.expected_m < p.rows_a ? p.expected_m : p.rows_a;
-        return launch_rows<Mode::Masked, PK>(tile_rows(expect, p.G, tiles_n, num_cus), p, num_cus, stream, config);
+        const Tile t = choose_tile(expect, 0, p.G, p.I, p.K, !p.q, false, num_cus);
+        return launch_tile<Mode::Masked, PK>(t, p, num_cus, stream, config);
     }
     case Mode::KGrouped: break;
     }
     return hipErrorInvalidValue;
 }
 
-size_t gated_workspace(int M, int I, int K, int num_cus) { return gated_small_workspace(M, I, K, num_cus); }
+size_t gated_workspace(int M, int I, int K, int num_cus) {
+    if (M <= kGatedSmallMaxM) return gated_small_workspace(M, I, K, num_cus);
+    if (I % 128 != 0) return 0;                    // no quantised output
+    const int rest = M - head_rows(M, I, num_cus);
+    return rest > 0 && choose_tile(rest, 0, 1, I, K, true, true, num_cus).cols < 128 ? (size_t)rest * I * sizeof(float) : 0;
+}
 
 hipError_t launch_gated(const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config) {
     if (gated_small_takes(p, num_cus)) return launch_gated_small(p, num_cus, stream, config);

@@ -276,20 +276,8 @@ __global__ void __launch_bounds__(64) gated_finish_kernel(GatedSmallArgs p) {
     if (in)
         *reinterpret_cast<uint2 *>(p.q + (int64_t)row * I + c) =
             uint2{encode4<PK>(v4f{h[0], h[1], h[2], h[3]}, d), encode4<PK>(v4f{h[4], h[5], h[6], h[7]}, d)};
-    if (in && (lane & 15) == 0) {
-        if constexpr (PK) {
-            // byte nb % 4 of the row's word; the last block clears the bytes past it
-            uint8_t *e = static_cast<uint8_t *>(p.sf) + ((int64_t)(nb / 4) * p.ld_sf + row) * 4;
-            e[nb & 3] = (uint8_t)(__float_as_uint(s) >> 23);
-            if (nb == nnb - 1)
-                for (int b = (nb & 3) + 1; b < 4; ++b) e[b] = 0;
-        } else {
-            static_cast<float *>(p.sf)[(int64_t)nb * p.ld_sf + row] = s;
-        }
-    }
+    if (in && (lane & 15) == 0) store_block_scale<PK>(static_cast<uint32_t *>(p.sf), p.ld_sf, row, nb, nnb, s);
 }
-
-constexpr int kSmallMaxM = 128;
 
 // Fragments per workgroup and K splits.  A workgroup reads all of A (of its K
 // share) for its 8 * nf columns, so above 16 rows two fragments are taken once
@@ -315,12 +303,12 @@ static SmallPlan small_plan(int M, int I, int K, bool quant, int num_cus) {
 
 // Scratch of a quantised output: the partial sums.  (Other outputs need none.)
 size_t gated_small_workspace(int M, int I, int K, int num_cus) {
-    if (M < 1 || M > kSmallMaxM || I % 128 != 0) return 0;
+    if (M < 1 || M > kGatedSmallMaxM || I % 128 != 0) return 0;
     return (size_t)small_plan(M, I, K, true, num_cus).splits * M * 2 * I * sizeof(float);
 }
 
 bool gated_small_takes(const GatedProblem &p, int num_cus) {
-    if (p.mode != Mode::Dense || p.rows_a > kSmallMaxM || (int64_t)p.rows_a * p.K >= (int64_t)1 << 31) return false;
+    if (p.mode != Mode::Dense || p.rows_a > kGatedSmallMaxM || (int64_t)p.rows_a * p.K >= (int64_t)1 << 31) return false;
     return !p.q || (p.ws && p.ws_bytes >= gated_small_workspace(p.rows_a, p.I, p.K, num_cus));
 }
 

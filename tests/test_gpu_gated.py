@@ -361,3 +361,105 @@ def test_workspace_reuse_streams_and_graph():
         assert torch.equal(h, f[0]) and torch.equal(q, f[1]) and torch.equal(sf, f[2])
         call(cases[1], ws)
         torch.cuda.synchronize()
+
+
+@pytest.fixture
+def cu_caps():
+    """Caps of the CU count: the tile that fills the CUs best changes with it, so one problem meets them all."""
+    yield (1, 3, 4, 8, 12, 16, 24, 40, 80, 200)
+    dg.set_num_cus(0)
+
+
+def tiles_of(config):
+    return {part.split()[0] for part in config.split("tile=")[1:]}
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_dense_every_tile(packed, cu_caps):
+    """One problem in each tile shape, all outputs, with scratch for the quantised output and without it; and a width
+    that is no multiple of a block."""
+    seen = {}
+    for M, I, K in ((300, 256, 4096), (301, 269, 640)):       # the second kernel pays where K is long
+        p = problem((), M, I, K, M, packed)
+        ld = p[1].shape[1]
+        ops = operands(p, packed)
+        gate, up = projections(*p)
+        quant = I % 128 == 0
+        for cus in cu_caps:
+            dg.set_num_cus(cus)
+            for ws in ("auto", None) if quant else ("auto",):
+                announce(f"gated tiles M={M} I={I} packed={packed} cus={cus} workspace={ws}")
+                o = Outputs((), M, I, ld, packed, quant)
+                dg.fp8_gated_gemm_nt(*ops, act="gelu", h=o.h, q=o.q, sf=o.sf, gu=o.gu, workspace=ws)
+                torch.cuda.synchronize()
+                o.guards()
+                sf = scales_of(o.sf[:, :M], packed, I // 128).T if quant else None
+                check_rows(f"cus={cus} {dg.last_config()}", o.gu, o.h, o.q, sf, I, gate, up, "gelu", packed)
+                seen.setdefault((I, ws), set()).update(tiles_of(dg.last_config()))
+    wide = {"256x256x128", "128x256x128", "64x256x128"}
+    narrow = {"128x128x128", "64x128x128", "64x64x128"}
+    assert seen[256, None] == wide
+    assert len(narrow & seen[256, "auto"]) >= 2 and narrow <= seen[269, "auto"] and wide <= seen[256, "auto"] | seen[269, "auto"]
+
+
+@pytest.mark.parametrize("counts", [[100, 0, 257, 129], [1, 2, 3, 4], [640]])
+@pytest.mark.parametrize("packed", [False, True])
+def test_contiguous_every_tile(counts, packed, cu_caps):
+    """The bf16 outputs of the contiguous layout, where narrow tiles serve too; NaN on the rows without data."""
+    I, K = 268, 640
+    idx = synth.contiguous_m_indices(counts)
+    M, G = idx.size, len(counts)
+    p = problem((), M, I, K, 70 + M, packed, (G,))
+    a, sfa, b, sfb = (x.copy() for x in p)
+    a[idx < 0] = 0x7F
+    if not packed:
+        sfa[:, idx < 0] = np.nan
+    ops = operands((a, sfa, b, sfb), packed)
+    pad = torch.from_numpy(idx < 0).cuda()
+    want = {e: projections(p[0][idx == e], p[1][:, idx == e], p[2][e], p[3][e]) for e in range(G) if counts[e]}
+    seen = set()
+    for cus in cu_caps:
+        dg.set_num_cus(cus)
+        announce(f"gated contiguous tiles {counts} packed={packed} cus={cus}")
+        o = Outputs((), M, I, M, packed, False)
+        dg.m_grouped_fp8_gated_gemm_nt_contiguous(*ops, dev(idx), act="silu", h=o.h, gu=o.gu)
+        torch.cuda.synchronize()
+        o.guards()
+        seen |= tiles_of(dg.last_config())
+        assert torch.all(o.h.view(torch.int16)[pad] == SENT) and torch.all(o.gu.view(torch.int16)[pad] == SENT)
+        for e, (gate, up) in want.items():
+            t = torch.from_numpy(np.flatnonzero(idx == e)).cuda()
+            check_rows(f"expert {e} cus={cus} {dg.last_config()}", o.gu[t], o.h[t], None, None, I, gate, up, "silu", packed)
+    assert {"128x256x128", "128x128x128"} <= seen and seen & {"64x128x128", "64x64x128"}
+
+
+@pytest.mark.parametrize("cap,mm", [(200, [200, 0, 77]), (300, [129, 300, -1]), (16, [1, 16, 9])])
+@pytest.mark.parametrize("packed", [False, True])
+def test_masked_every_tile(cap, mm, packed, cu_caps):
+    I, K, G = 268, 640, len(mm)
+    p = problem((G,), cap, I, K, cap, packed, (G,))
+    a, sfa, b, sfb = (x.copy() for x in p)
+    rows = [min(max(m, 0), cap) for m in mm]
+    for g in range(G):
+        a[g, rows[g]:] = 0x7F
+        if not packed:
+            sfa[g, :, rows[g]:] = np.nan
+    ops = operands((a, sfa, b, sfb), packed)
+    counts = torch.tensor(mm, dtype=torch.int32, device="cuda")
+    want = [projections(p[0][g, :rows[g]], p[1][g][:, :rows[g]], p[2][g], p[3][g]) if rows[g] else None for g in range(G)]
+    seen = set()
+    for cus in cu_caps:
+        dg.set_num_cus(cus)
+        announce(f"gated masked tiles {mm} packed={packed} cus={cus}")
+        o = Outputs((G,), cap, I, (cap + 3) // 4 * 4, packed, False)
+        dg.m_grouped_fp8_gated_gemm_nt_masked(*ops, counts, act="silu", h=o.h, gu=o.gu)
+        torch.cuda.synchronize()
+        o.guards()
+        seen |= tiles_of(dg.last_config())
+        for g in range(G):
+            assert torch.all(o.h[g, rows[g]:].contiguous().view(torch.int16) == SENT)
+            assert torch.all(o.gu[g, rows[g]:].contiguous().view(torch.int16) == SENT)
+            if rows[g]:
+                check_rows(f"group {g} cus={cus} {dg.last_config()}", o.gu[g, :rows[g]], o.h[g, :rows[g]], None, None, I,
+                           *want[g], "silu", packed)
+    assert seen & {"128x128x128", "64x128x128", "64x64x128"}
