@@ -527,7 +527,7 @@ int64_t dg_get_rmsnorm_backward_workspace_size(int rows, int K);
  *   or too few bytes, a kernel that needs none (and is slower there) computes
  *   the same outputs.
  * Errors: DG_ERR_NULL; DG_ERR_SHAPE (M < 0; I < 1; K < 128 or K % 128; q with
- * I % 128; 2*I*K or the bytes of sfa reaching 2^31); DG_ERR_ARG (act);
+ * I % 128; 2*I*K, 256*K or the bytes of sfa reaching 2^31); DG_ERR_ARG (act);
  * DG_ERR_ALIGN.
  */
 int dg_fp8_gated_gemm_nt(const uint8_t *a, const float *sfa, int ld_sfa,
@@ -591,8 +591,8 @@ int dg_m_grouped_fp8_gated_gemm_nt_masked_ue8m0_packed(const uint8_t *a, const u
  *   ht [.. as qt ..][I] E4M3, sfht [ceil(rows/128)][I]   the same of h =
  *       act(gate) * up, for the weight gradient of the projection that follows
  * The _ue8m0 form rounds every scale up to a power of two.
- * Errors: DG_ERR_NULL; DG_ERR_SHAPE (rows < 0; I < 128 or I % 128); DG_ERR_ARG
- * (act); DG_ERR_ALIGN (m_indices: 4 bytes, the others 16; ld_sf < rows or
+ * Errors: DG_ERR_NULL; DG_ERR_SHAPE (rows < 0; I < 128, I % 128, or 512*I
+ * reaching 2^31); DG_ERR_ARG (act); DG_ERR_ALIGN (m_indices: 4 bytes, the others 16; ld_sf < rows or
  * ld_sf % 4).
  */
 int dg_gated_backward_quantize_e4m3(const uint16_t *gu, const uint16_t *dh, int act, const int32_t *m_indices,

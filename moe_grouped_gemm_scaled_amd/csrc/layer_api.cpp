@@ -52,7 +52,9 @@ struct GatedOut {
 int gated_check(const void *a, const void *sfa, const void *b, const void *sfb, int act, const GatedOut &o, int rows,
                 int ld_sfa, int I, int K) {
     if (rows < 0 || I < 1 || K < 128 || K % 128 != 0) return DG_ERR_SHAPE;
-    if (2 * (int64_t)I * K >= kOffsetLimit || (int64_t)(K / 128) * ld_sfa * 4 >= kOffsetLimit) return DG_ERR_SHAPE;
+    if (2 * (int64_t)I * K >= kOffsetLimit || 256 * (int64_t)K >= kOffsetLimit ||
+        (int64_t)(K / 128) * ld_sfa * 4 >= kOffsetLimit)
+        return DG_ERR_SHAPE;
     if (o.q && I % 128 != 0) return DG_ERR_SHAPE;
     if (!act_ok(act)) return DG_ERR_ARG;
     if (rows > 0 && (!a || !sfa || !b || !sfb || (!o.h && !o.q) || (o.q && !o.sf))) return DG_ERR_NULL;
@@ -119,7 +121,7 @@ int gated_masked(const uint8_t *a, const void *sfa, const uint8_t *b, const void
 int gated_bwd_impl(const uint16_t *gu, const uint16_t *dh, int act, const int32_t *m_indices, uint16_t *dgu, uint8_t *q,
                    float *sf, int ld_sf, uint8_t *qt, float *sft, uint8_t *ht, float *sfht, int rows, int I,
                    void *stream, bool ue8m0) {
-    if (rows < 0 || I < 128 || I % 128 != 0) return DG_ERR_SHAPE;
+    if (rows < 0 || I < 128 || I % 128 != 0 || 512 * (int64_t)I >= kOffsetLimit) return DG_ERR_SHAPE;
     if (!act_ok(act)) return DG_ERR_ARG;
     if (rows > 0 && (!gu || !dh || (!dgu && !q && !qt && !ht) || (q && !sf) || (qt && !sft) || (ht && !sfht)))
         return DG_ERR_NULL;
@@ -190,7 +192,9 @@ int dg_rmsnorm_backward(const void *dy, int dy_type, const void *h, int h_type, 
 }
 
 int64_t dg_get_gated_workspace_size(int M, int I, int K) {
-    if (M < 0 || I < 1 || K < 128 || K % 128 != 0 || 2 * (int64_t)I * K >= kOffsetLimit) return DG_ERR_SHAPE;
+    if (M < 0 || I < 1 || K < 128 || K % 128 != 0 || 2 * (int64_t)I * K >= kOffsetLimit ||
+        256 * (int64_t)K >= kOffsetLimit)
+        return DG_ERR_SHAPE;
     int cus = 0;
     const int st = dg::current_device_cus(cus);
     if (st != DG_OK) return st;

@@ -171,3 +171,15 @@ def test_reference_activations():
     for kind in ("silu", "gelu"):
         d = (layer_helpers.act(g + 1e-6, kind) - layer_helpers.act(g - 1e-6, kind)) / 2e-6
         assert np.max(np.abs(d - layer_helpers.act_grad(g, kind))) < 1e-8
+
+
+def test_limits_of_32_bit_offsets(lib):
+    """Sizes whose offsets inside a tile would pass 32 bits."""
+    K = 1 << 23
+    assert lib.dg_get_gated_workspace_size(1, 1, K) == SHAPE
+    c = Call(lib.dg_fp8_gated_gemm_nt, a=P, sfa=P, ld_sfa=4, b=P, sfb=P, act=0, gu=None, h=P, q=None, sf=None, ld_sf=4,
+             M=1, I=1, K=K, workspace=None, workspace_bytes=0, stream=None)
+    refused(c, SHAPE)
+    c = Call(lib.dg_gated_backward_quantize_e4m3, gu=P, dh=P, act=0, m_indices=None, dgu=P, q=None, sf=None, ld_sf=4,
+             qt=None, sft=None, ht=None, sfht=None, rows=1, I=1 << 22, stream=None)
+    refused(c, SHAPE)
