@@ -57,19 +57,6 @@ __device__ __forceinline__ void dma_lds16(__amdgpu_buffer_rsrc_t r, uint8_t *dst
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, DG_LDS(dst), 16, voffset, soffset, 0, 0);
 }
 
-// One 4-byte-per-lane buffer load into LDS (256 B per wave at `dst`).
-__device__ __forceinline__ void dma_lds4(__amdgpu_buffer_rsrc_t r, uint8_t *dst, int voffset, int soffset) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, DG_LDS(dst), 4, voffset, soffset, 0, 0);
-}
-
-// Waits for this wave's LDS reads, so that a DMA may overwrite what they
-// read; a stage that only one wave uses needs no barrier besides.
-__device__ __forceinline__ void lds_reads_done() {
-    __builtin_amdgcn_s_waitcnt(0xc07f);
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // MFMA fragment of an operand stored MN-major in LDS: rows are K (PITCH
 // bytes each, 16-byte columns XOR-swizzled by (row & 7)), columns are M (or
 // N).  gfx950's ds_read_b64_tr_b8 gathers, in each group of 16 lanes, byte
@@ -97,106 +84,6 @@ __device__ __forceinline__ v8i read_frag_tr(const uint8_t *p) {
 __device__ __forceinline__ int opaque_offset(int x) {
     asm("" : "+v"(x));
     return x;
-}
-
-// Contiguous layout with 256-row tiles: the u-th "unit" of 256 rows.  Units
-// start at every other 128-row block of an expert's segment (its first
-// block, its third, ...), so a unit never mixes two experts' rows; the last
-// unit of a segment with an odd number of blocks holds 128 of them (its
-// other rows are not stored).  Every lane of the wave gets the unit's first
-// block, or -1 if there are fewer units.  The segments are read from the
-// expert index of each block's first row (segments are 128-row aligned),
-// four blocks per lane at a time, all loads in flight together.
-__device__ __forceinline__ int contig_unit_block(const int32_t *idx, int nblocks, int u) {
-    const int lane = threadIdx.x & 63;
-    int prev_e = -1;     // expert of the block before this round (none: -1)
-    int seg = -1;        // first block of the segment running into this round
-    int count = 0;       // units before this round
-    for (int base = 0; base < nblocks; base += 256) {
-        int e[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int b = base + 64 * q + lane;
-            e[q] = b < nblocks ? idx[(int64_t)b * 128] : -1;
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int b = base + 64 * q + lane;
-            int ep = __shfl_up(e[q], 1);
-            if (lane == 0) ep = prev_e;
-            const bool start = e[q] >= 0 && e[q] != ep;
-            int sg = start ? b : -1;                  // inclusive max-scan of segment starts
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int t = __shfl_up(sg, o);
-                if (lane >= o) sg = sg > t ? sg : t;
-            }
-            sg = sg > seg ? sg : seg;
-            const bool unit = e[q] >= 0 && ((b - sg) & 1) == 0;
-            const uint64_t m = __ballot(unit);
-            const int n = __popcll(m);
-            if (u < count + n) {
-                const int rank = __popcll(m & ((1ull << lane) - 1ull));
-                const uint64_t hit = __ballot(unit && rank == u - count);
-                return base + 64 * q + __ffsll((unsigned long long)hit) - 1;
-            }
-            count += n;
-            prev_e = __shfl(e[q], 63);
-            seg = __shfl(sg, 63);
-        }
-    }
-    return -1;
-}
-
-// Expert indices of blocks base + 64 q + lane (-1 past the end): one round of
-// contig_scan, all loads in flight together.
-struct ContigBlocks {
-    int e[4];
-};
-__device__ __forceinline__ ContigBlocks contig_load(const int32_t *idx, int nblocks, int base) {
-    ContigBlocks r;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int b = base + 64 * q + (int)(threadIdx.x & 63);
-        r.e[q] = b < nblocks ? idx[(int64_t)b * 128] : -1;
-    }
-    return r;
-}
-
-// The walk of contig_unit_block to its end: returns the first block of unit u
-// (-1 for none, or u < 0) and leaves the number of units in `units`.  `first`:
-// the first round's blocks, which two walks can share.
-__device__ __forceinline__ int contig_scan(const int32_t *idx, int nblocks, const ContigBlocks &first, int u, int &units) {
-    const int lane = threadIdx.x & 63;
-    const uint64_t upto = ~0ull >> (63 - lane);   // this lane and those before it
-    int prev_e = -1;     // expert of the block before this step (none: -1)
-    int seg = -1;        // first block of the segment running into this step
-    int count = 0, found = -1;
-    for (int base = 0; base < nblocks; base += 256) {
-        ContigBlocks r = first;
-        if (base > 0) r = contig_load(idx, nblocks, base);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int e = r.e[q], b0 = base + 64 * q;
-            int ep = __shfl_up(e, 1);
-            if (lane == 0) ep = prev_e;
-            const uint64_t starts = __ballot(e >= 0 && e != ep);
-            const int sg = starts & upto ? b0 + 63 - __clzll((long long)(starts & upto)) : seg;
-            const bool unit = e >= 0 && ((b0 + lane - sg) & 1) == 0;
-            const uint64_t m = __ballot(unit);
-            const int n = __popcll(m);
-            if (u >= count && u < count + n) {
-                const int rank = __popcll(m & (upto >> 1));
-                const uint64_t hit = __ballot(unit && rank == u - count);
-                found = b0 + __ffsll((unsigned long long)hit) - 1;
-            }
-            count += n;
-            prev_e = __shfl(e, 63);
-            seg = __shfl(sg, 63);
-        }
-    }
-    units = count;
-    return found;
 }
 
 // Steps U, U+1, .. of one round of the K loop, step U + i running only when

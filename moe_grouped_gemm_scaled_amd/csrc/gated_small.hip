@@ -24,9 +24,9 @@
 #include <stdio.h>
 
 #include "dg_act.h"
+#include "dg_gated.h"
 #include "dg_internal.h"
 #include "dg_layer.h"
-#include "dg_pipeline.h"
 #include "dg_quant.h"
 #include "dg_rows.h"
 

@@ -72,6 +72,55 @@ struct PipeParams {
     float *d32;
 };
 
+// Contiguous layout with 256-row tiles: the u-th "unit" of 256 rows.  Units
+// start at every other 128-row block of an expert's segment (its first
+// block, its third, ...), so a unit never mixes two experts' rows; the last
+// unit of a segment with an odd number of blocks holds 128 of them (its
+// other rows are not stored).  Every lane of the wave gets the unit's first
+// block, or -1 if there are fewer units.  The segments are read from the
+// expert index of each block's first row (segments are 128-row aligned),
+// four blocks per lane at a time, all loads in flight together.
+__device__ __forceinline__ int contig_unit_block(const int32_t *idx, int nblocks, int u) {
+    const int lane = threadIdx.x & 63;
+    int prev_e = -1;     // expert of the block before this round (none: -1)
+    int seg = -1;        // first block of the segment running into this round
+    int count = 0;       // units before this round
+    for (int base = 0; base < nblocks; base += 256) {
+        int e[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int b = base + 64 * q + lane;
+            e[q] = b < nblocks ? idx[(int64_t)b * 128] : -1;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int b = base + 64 * q + lane;
+            int ep = __shfl_up(e[q], 1);
+            if (lane == 0) ep = prev_e;
+            const bool start = e[q] >= 0 && e[q] != ep;
+            int sg = start ? b : -1;                  // inclusive max-scan of segment starts
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int t = __shfl_up(sg, o);
+                if (lane >= o) sg = sg > t ? sg : t;
+            }
+            sg = sg > seg ? sg : seg;
+            const bool unit = e[q] >= 0 && ((b - sg) & 1) == 0;
+            const uint64_t m = __ballot(unit);
+            const int n = __popcll(m);
+            if (u < count + n) {
+                const int rank = __popcll(m & ((1ull << lane) - 1ull));
+                const uint64_t hit = __ballot(unit && rank == u - count);
+                return base + 64 * q + __ffsll((unsigned long long)hit) - 1;
+            }
+            count += n;
+            prev_e = __shfl(e[q], 63);
+            seg = __shfl(sg, 63);
+        }
+    }
+    return -1;
+}
+
 // Swizzle of the 16-byte columns of K row r of an MN-major LDS tile with CPR
 // columns per row.  (r & 7) spreads the eight rows that one 16-lane group of
 // a transposing read touches over eight column positions.  In 256-byte rows
