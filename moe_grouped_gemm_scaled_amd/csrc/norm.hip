@@ -333,18 +333,23 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *__restric
     }
 }
 
-// Workgroups of the backward pass: two per CU at most, each with two rows or
-// more, so that their partial rows of dw stay small next to the rows (333 rows
-// of 2048: 5.6 us, 7.5 with four rows or more; one row or more changes
-// nothing).
-static int bwd_groups(int rows, int num_cus) {
-    const int64_t most = 2 * (int64_t)num_cus;
-    const int64_t g = ((int64_t)rows + 1) / 2;
+// Workgroups of the backward pass.  One for a few short rows: its dw needs no
+// second kernel, whose launch costs the host 2.6 us (8 rows of 1536: 8.4 us
+// against 3.2 + 2.2 and a gap).  A row each up to as many rows as CUs (87 rows
+// of 16000, fp32: 12.7 against 16.4 us with two), two rows or more above, so
+// that the partial rows of dw stay small next to the rows (500 rows of 7168:
+// 11.3 + 4.7 against 13.6 + 5.5 us with one; 333 of 2048: 5.6 against 7.5 us
+// with four).  Two workgroups per CU at most, one above 8192 columns, where two
+// do not fit (1059 rows of 10240, fp32: 38.9 against 44.3 us).
+static int bwd_groups(int rows, int K, int num_cus) {
+    if ((int64_t)rows * K < 16384) return 1;
+    const int64_t most = K > 8192 ? num_cus : 2 * (int64_t)num_cus;
+    const int64_t g = rows <= num_cus ? rows : ((int64_t)rows + 1) / 2;
     return (int)(g < most ? (g > 0 ? g : 1) : most);
 }
 
 size_t rmsnorm_bwd_workspace(int rows, int K, int num_cus) {
-    const int g = bwd_groups(rows, num_cus);
+    const int g = bwd_groups(rows, K, num_cus);
     return g > 1 ? (size_t)g * K * sizeof(float) : 0;
 }
 
@@ -363,7 +368,7 @@ static hipError_t launch_bwd_t(const RmsNormBwdProblem &p, int groups, hipStream
 
 template <typename TH, typename TY, typename TW>
 static hipError_t launch_bwd_k(const RmsNormBwdProblem &p, int num_cus, hipStream_t stream) {
-    const int g = bwd_groups(p.rows, num_cus);
+    const int g = bwd_groups(p.rows, p.K, num_cus);
     const int n = (p.K + 511) / 512;
     if (n <= 1) return launch_bwd_t<TH, TY, TW, 1, 1>(p, g, stream);
     if (n <= 2) return launch_bwd_t<TH, TY, TW, 1, 2>(p, g, stream);

@@ -463,3 +463,32 @@ def test_masked_every_tile(cap, mm, packed, cu_caps):
                 check_rows(f"group {g} cus={cus} {dg.last_config()}", o.gu[g, :rows[g]], o.h[g, :rows[g]], None, None, I,
                            *want[g], "silu", packed)
     assert seen & {"128x128x128", "64x128x128", "64x64x128"}
+
+
+# rows on both sides of every fragment count, few and many columns, K long enough that the sums go through scratch
+SMALL_Q = [(1, 128, 1152), (15, 256, 2048), (17, 384, 1280), (32, 4224, 1152), (33, 256, 1408), (48, 4224, 1152), (64, 640, 1152),
+           (65, 128, 3200), (100, 2048, 1152), (127, 256, 1280), (128, 4224, 1152)]
+
+
+@pytest.mark.parametrize("M,I,K", SMALL_Q)
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("cus", [0, 24])
+def test_dense_few_rows_quantised(M, I, K, packed, cus):
+    announce(f"gated few rows M={M} I={I} K={K} packed={packed} cus={cus}")
+    p = problem((), M, I, K, M + I + K, packed)
+    ld = p[1].shape[1]
+    ops = operands(p, packed)
+    dg.set_num_cus(cus)
+    try:
+        assert dg.get_gated_workspace_size(M, I, K) > 0
+        for all_outputs in (True, False):
+            o = Outputs((), M, I, ld, packed, True)
+            dg.fp8_gated_gemm_nt(*ops, act="gelu", q=o.q, sf=o.sf, **(dict(h=o.h, gu=o.gu) if all_outputs else {}))
+            torch.cuda.synchronize()
+            assert "family=gated_small" in dg.last_config()
+            o.guards()
+            gate, up = projections(*p)
+            check_rows(f"M={M} I={I} K={K} {dg.last_config()}", o.gu if all_outputs else None, o.h if all_outputs else None, o.q,
+                       scales_of(o.sf[:, :M], packed, I // 128).T, I, gate, up, "gelu", packed)
+    finally:
+        dg.set_num_cus(0)
