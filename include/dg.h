@@ -592,8 +592,8 @@ int dg_m_grouped_fp8_gated_gemm_nt_masked_ue8m0_packed(const uint8_t *a, const u
  *       act(gate) * up, for the weight gradient of the projection that follows
  * The _ue8m0 form rounds every scale up to a power of two.
  * Errors: DG_ERR_NULL; DG_ERR_SHAPE (rows < 0; I < 128, I % 128, or 512*I
- * reaching 2^31); DG_ERR_ARG (act); DG_ERR_ALIGN (m_indices: 4 bytes, the others 16; ld_sf < rows or
- * ld_sf % 4).
+ * reaching 2^31); DG_ERR_ARG (act); DG_ERR_ALIGN (m_indices: 4 bytes, the
+ * others 16; ld_sf < rows or ld_sf % 4).
  */
 int dg_gated_backward_quantize_e4m3(const uint16_t *gu, const uint16_t *dh, int act, const int32_t *m_indices,
                                     uint16_t *dgu, uint8_t *q, float *sf, int ld_sf,

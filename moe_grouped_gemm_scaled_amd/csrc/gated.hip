@@ -44,19 +44,13 @@ struct GatedArgs {
     void *sf;
     int rows_a, I, K, ld_sfa, ld_sf, G, act;
     int tiles_m, tiles_n, gm;
-    int part, cus;             // contiguous: which rows this launch takes (ContigPart)
+    int cus;                   // contiguous, 256-row tiles: the CUs that a round fills
     int sa_cols;               // columns of sfa from the first row on (ld_sfa, less the rows before it)
     float *hq;                 // tiles of fewer than 128 columns: h of a quantised output in fp32, [rows][I]
 };
 
-// The contiguous layout can take two launches: 256-row units that fill the CUs
-// a whole number of times, then the remaining rows in 128-row blocks, when
-// those fit the CUs at once: a last, partly filled round of 256-row tiles costs
-// as much as a full one.  How many units there are is known on the device
-// only, so both launches work it out from m_indices.
-enum ContigPart : int { kAllRows = 0, kHead = 1, kTail = 2 };
-
-// Units of the head launch: all `units`, or those of the full rounds.
+// Contiguous layout in 256-row units: those of the full rounds over the CUs, or
+// all of them, where the rest would not find room at once in 128-row blocks.
 __device__ __forceinline__ int head_units(int units, int tiles_n, int cus) {
     const int64_t tiles = (int64_t)units * tiles_n;
     const int full = (int)(tiles / cus * cus / tiles_n);
@@ -71,9 +65,16 @@ __device__ __forceinline__ int staged(int r, int c) {
     return (r * CPR + (c ^ (r & (CPR - 1)))) * 16;
 }
 
+// Bytes of a stage: A rows, B rows, and 1 KB each for the scales of A, of B and
+// the scale loads of the waves that fetch none.
+constexpr int stage_bytes(int bm, int bh) { return (bm + 2 * bh) * kKBlock + 3 * 1024; }
+
+// One tile: rows m0 .. m0 + BM - 1 (of group grp), columns BH * tn .. +BH-1.
+// The stages are separate LDS objects, so that the compiler can tell reads of
+// one from DMA into another.
 template <int BM, int BH, int NST, Mode MODE, bool PK>
-__global__ void __launch_bounds__(512, BH == 32 ? 4 : 2)   // waves per SIMD: two workgroups of the smallest tile share a CU
-gated_kernel(GatedArgs p) {
+__device__ __forceinline__ void gated_tile(const GatedArgs &p, const int m0, const int tn, const int grp, uint8_t *stage0,
+                                           uint8_t *stage1, uint8_t *stage2, float *row_max, uint8_t *of_expert) {
     constexpr int BN = 2 * BH;                    // B rows of a tile
     constexpr int NW = 8, WGN = BN >= 128 ? 4 : BN / 32, WGM = NW / WGN;   // waves
     constexpr int TM = BM / WGM, TN = BN / WGN;   // wave tile
@@ -86,70 +87,25 @@ gated_kernel(GatedArgs p) {
     constexpr int OFF_SB = OFF_SA + 1024;         // gate, up: 16 bytes of sfb from K block kb
     constexpr int OFF_JUNK = OFF_SB + 1024;       // scale loads of the waves that fetch none (zeros)
     constexpr int STAGE = OFF_JUNK + 1024;
+    static_assert(STAGE == stage_bytes(BM, BH), "stage");
     constexpr int DA = BM / (8 * NW), DB = BN / (8 * NW);   // 1-KB LDS-DMA chunks per wave per K block
     constexpr int PER_BLOCK = DA + DB + 1;
-    static_assert(NST >= 2 && NST <= 4 && NST * STAGE + BM * (WGN * 4 + 1) <= 160 * 1024, "LDS");
+    static_assert(NST >= 2 && NST <= 3 && NST * STAGE + BM * (WGN * 4 + 1) <= 160 * 1024, "LDS");
     static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM / 4 <= 64 && NW >= 2, "DMA chunks");
     static_assert((NST - 2) * PER_BLOCK < 64, "vmcnt immediate");
     static_assert(TH % 16 == 0 && BM * BH * 2 <= STAGE, "a staged output tile fits one stage");
 
-    __shared__ __attribute__((aligned(16))) uint8_t stage0[STAGE];
-    __shared__ __attribute__((aligned(16))) uint8_t stage1[STAGE];
-    __shared__ __attribute__((aligned(16))) uint8_t stage2[NST > 2 ? STAGE : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t stage3[NST > 3 ? STAGE : 16];
-    __shared__ float row_max[WGN][BH == 128 ? BM : 1];
     auto stage_of = [&](auto sc) __attribute__((always_inline)) -> uint8_t * {
         constexpr int s = decltype(sc)::value;
         if constexpr (s == 0) return stage0;
         else if constexpr (s == 1) return stage1;
-        else if constexpr (s == 2) return stage2;
-        else return stage3;
+        else return stage2;
     };
 
     const int K = p.K, I = p.I;
     const int nkb = K / kKBlock;
     const int nnb = (I + 127) / 128;
     const int nkw = PK ? (nkb + 3) / 4 : nkb;
-    const int tiles_per_group = p.tiles_m * p.tiles_n;
-    // contiguous: the first row block and the number of row tiles of this launch
-    int tiles_m = p.tiles_m, block0 = 0;
-    ContigBlocks blocks;
-    const int nblocks = p.rows_a / 128;
-    if constexpr (MODE == Mode::Contig) {
-        if (BM == 256 || p.part != kAllRows) blocks = contig_load(p.idx, nblocks, 0);
-        if (p.part != kAllRows) {
-            int units = 0;
-            contig_scan(p.idx, nblocks, blocks, -1, units);
-            const int head = head_units(units, p.tiles_n, p.cus);
-            if (BM == 256) {
-                tiles_m = head;
-            } else {
-                if (head >= units) return;         // no tail: uniform exit
-                int u = 0;
-                block0 = head > 0 ? contig_scan(p.idx, nblocks, blocks, head, u) : 0;
-                tiles_m = (nblocks - block0) * 128 / BM;
-            }
-        }
-        tiles_m = __builtin_amdgcn_readfirstlane(tiles_m);
-        block0 = __builtin_amdgcn_readfirstlane(block0);
-    }
-    const int total = MODE == Mode::Contig ? tiles_m * p.tiles_n : (int)gridDim.x;
-    if ((int)blockIdx.x >= total) return;          // uniform exit
-    int t_lin = xcd_remap(blockIdx.x, total);
-    int grp = 0;
-    if (MODE == Mode::Masked) {
-        grp = t_lin / tiles_per_group;
-        t_lin -= grp * tiles_per_group;
-    }
-    int tm, tn;
-    raster(t_lin, tiles_m, p.tiles_n, p.gm, tm, tn);
-    int m0 = block0 * 128 + tm * BM;
-    if constexpr (MODE == Mode::Contig && BM == 256) {
-        int units = 0;
-        const int ub = __builtin_amdgcn_readfirstlane(contig_scan(p.idx, nblocks, blocks, tm, units));
-        if (ub < 0) return;                        // no such unit: uniform exit
-        m0 = ub * 128;
-    }
     const int n0 = tn * BH;
 
     const uint8_t *A = p.a;
@@ -344,7 +300,6 @@ gated_kernel(GatedArgs p) {
     // output row is row_base + m0 + r).
     // Contiguous: a row of the expert, looked up once per row (looked up with
     // every 16 bytes stored it took 17 us of a 136 us round).
-    __shared__ uint8_t of_expert[MODE == Mode::Contig ? BM : 1];
     if constexpr (MODE == Mode::Contig) {
         if (tid < BM) of_expert[tid] = row_id == expert;
         lds_barrier();
@@ -445,15 +400,15 @@ gated_kernel(GatedArgs p) {
             });
             m = fmaxf(m, __shfl_xor(m, 16));
             m = fmaxf(m, __shfl_xor(m, 32));
-            if (g4 == 0) row_max[wn][wm * TM + 16 * i + l16] = m;
+            if (g4 == 0) row_max[wn * BM + wm * TM + 16 * i + l16] = m;
         });
         lds_barrier();
         static_for<SM>([&](auto ic) __attribute__((always_inline)) {
             constexpr int i = decltype(ic)::value;
             const int r = wm * TM + 16 * i + l16;
-            float m = row_max[0][r];
+            float m = row_max[r];
 #pragma unroll
-            for (int x = 1; x < WGN; ++x) m = fmaxf(m, row_max[x][r]);
+            for (int x = 1; x < WGN; ++x) m = fmaxf(m, row_max[x * BM + r]);
             const float s = block_scale<PK>(m);
             const BlockDivisor d = block_divisor<PK>(s);
             static_for<SH>([&](auto jc) __attribute__((always_inline)) {
@@ -471,6 +426,68 @@ gated_kernel(GatedArgs p) {
                 *reinterpret_cast<v4i *>(p.q + (row0 + r) * I + n0 + 16 * c) =
                     *reinterpret_cast<const v4i *>(stage1 + staged<8>(r, c));
         }
+    }
+}
+
+// One tile per workgroup, in all layouts.
+template <int BM, int BH, int NST, Mode MODE, bool PK>
+__global__ void __launch_bounds__(512, BH == 32 ? 4 : 2)   // waves per SIMD: two workgroups of the smallest tile share a CU
+gated_kernel(GatedArgs p) {
+    constexpr int STAGE = stage_bytes(BM, BH);
+    __shared__ __attribute__((aligned(16))) uint8_t stage0[STAGE];
+    __shared__ __attribute__((aligned(16))) uint8_t stage1[STAGE];
+    __shared__ __attribute__((aligned(16))) uint8_t stage2[NST > 2 ? STAGE : 16];
+    __shared__ float row_max[BH == 128 ? 4 * BM : 1];
+    __shared__ uint8_t of_expert[MODE == Mode::Contig ? BM : 1];
+    const int tiles_per_group = p.tiles_m * p.tiles_n;
+    int t_lin = xcd_remap(blockIdx.x, gridDim.x);
+    int grp = 0;
+    if (MODE == Mode::Masked) {
+        grp = t_lin / tiles_per_group;
+        t_lin -= grp * tiles_per_group;
+    }
+    int tm, tn;
+    raster(t_lin, p.tiles_m, p.tiles_n, p.gm, tm, tn);
+    gated_tile<BM, BH, NST, MODE, PK>(p, tm * BM, tn, grp, stage0, stage1, stage2, row_max, of_expert);
+}
+
+// Contiguous layout, many rows: tiles of 256-row units for the full rounds over
+// the CUs, then the remaining rows in 128-row blocks, when those fit the CUs at
+// once: a last, partly filled round of 256-row tiles costs as much as a full
+// one.  How many units there are is known on the device only, so every
+// workgroup works out its tile from m_indices.  In one launch the blocks fill
+// the CUs as the units' tiles end, of which those with one block of rows are
+// early.
+template <bool PK>
+__global__ void __launch_bounds__(512, 2) gated_units_kernel(GatedArgs p) {
+    constexpr int STAGE = stage_bytes(256, 128);
+    __shared__ __attribute__((aligned(16))) uint8_t stage0[STAGE];
+    __shared__ __attribute__((aligned(16))) uint8_t stage1[STAGE];
+    __shared__ float row_max[4 * 256];
+    __shared__ uint8_t of_expert[256];
+    const int nblocks = p.rows_a / 128;
+    const ContigBlocks blocks = contig_load(p.idx, nblocks, 0);
+    int units = 0;
+    contig_scan(p.idx, nblocks, blocks, -1, units);
+    units = __builtin_amdgcn_readfirstlane(units);
+    const int head = head_units(units, p.tiles_n, p.cus);
+    const int head_tiles = head * p.tiles_n, tail_m = 2 * (units - head);
+    int tm, tn;
+    if ((int)blockIdx.x < head_tiles) {
+        raster(xcd_remap(blockIdx.x, head_tiles), head, p.tiles_n, p.gm, tm, tn);
+        const int b = __builtin_amdgcn_readfirstlane(contig_scan(p.idx, nblocks, blocks, tm, units));
+        gated_tile<256, 128, 2, Mode::Contig, PK>(p, b * 128, tn, 0, stage0, stage1, nullptr, row_max, of_expert);
+    } else {
+        const int t = (int)blockIdx.x - head_tiles;
+        if (t >= tail_m * p.tiles_n) return;       // uniform exit
+        raster(xcd_remap(t, tail_m * p.tiles_n), tail_m, p.tiles_n, p.gm, tm, tn);
+        int b = __builtin_amdgcn_readfirstlane(contig_scan(p.idx, nblocks, blocks, head + tm / 2, units));
+        if (tm & 1) {
+            // the unit's second block, where it has one
+            if (b + 1 >= nblocks || p.idx[((int64_t)b + 1) * 128] != p.idx[(int64_t)b * 128]) return;
+            b += 1;
+        }
+        gated_tile<128, 128, 2, Mode::Contig, PK>(p, b * 128, tn, 0, stage0, stage1, nullptr, row_max, of_expert);
     }
 }
 
@@ -496,32 +513,45 @@ __global__ void __launch_bounds__(256) gated_encode_kernel(GatedArgs p) {
     if (lane16 == 0) store_block_scale<PK>(static_cast<uint32_t *>(p.sf), p.ld_sf, row, nb, nnb, s);
 }
 
-template <int BM, int BH, int NST, Mode MODE, bool PK>
-static hipError_t launch_t(const GatedProblem &p, int num_cus, ContigPart part, hipStream_t stream,
-                           std::string &config) {
-    GatedArgs k{p.a, p.sfa, p.b, p.sfb, p.idx, p.gu, p.h, p.q, p.sf, p.rows_a, p.I, p.K, p.ld_sfa, p.ld_sf, p.G, p.act,
-                0, 0, 4, part, num_cus, p.ld_sfa - p.row0, BH < 128 && p.q ? static_cast<float *>(p.ws) : nullptr};
-    k.tiles_m = (p.rows_a + BM - 1) / BM;
-    // contiguous 256-row units: at most one per 256 rows plus one per expert segment
-    if (MODE == Mode::Contig && BM == 256) k.tiles_m = p.rows_a / 256 + p.G + 1;
-    k.tiles_n = (p.I + BH - 1) / BH;
-    int64_t grid = (int64_t)k.tiles_m * k.tiles_n * (MODE == Mode::Masked ? p.G : 1);
-    if (part == kTail) {
-        // at most half the CUs' worth of 256-row units, two blocks each, and
-        // the padding blocks behind them, which exit
-        k.tiles_m = p.rows_a / BM;
-        grid = (int64_t)k.tiles_m * k.tiles_n;
-    }
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+static GatedArgs args_of(const GatedProblem &p, int bm, int bh, int num_cus) {
+    return {p.a, p.sfa, p.b, p.sfb, p.idx, p.gu, p.h, p.q, p.sf, p.rows_a, p.I, p.K, p.ld_sfa, p.ld_sf, p.G, p.act,
+            (p.rows_a + bm - 1) / bm, (p.I + bh - 1) / bh, 4, num_cus, p.ld_sfa - p.row0,
+            bh < 128 && p.q ? static_cast<float *>(p.ws) : nullptr};
+}
+
+static void describe(std::string &config, Mode mode, const char *tile, int stages, int64_t grid, bool packed) {
     char buf[160];
-    snprintf(buf, sizeof buf, "%sfamily=gated mode=%d tile=%dx%dx128 stages=%d grid=%lld%s",
-             config.empty() ? "" : " + ", (int)MODE, BM, 2 * BH, NST, (long long)grid, PK ? " scales=ue8m0_packed" : "");
+    snprintf(buf, sizeof buf, "%sfamily=gated mode=%d %s stages=%d grid=%lld%s", config.empty() ? "" : " + ", (int)mode,
+             tile, stages, (long long)grid, packed ? " scales=ue8m0_packed" : "");
     config += buf;
+}
+
+template <int BM, int BH, int NST, Mode MODE, bool PK>
+static hipError_t launch_t(const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config) {
+    const GatedArgs k = args_of(p, BM, BH, num_cus);
+    const int64_t grid = (int64_t)k.tiles_m * k.tiles_n * (MODE == Mode::Masked ? p.G : 1);
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    char tile[32];
+    snprintf(tile, sizeof tile, "tile=%dx%dx128", BM, 2 * BH);
+    describe(config, MODE, tile, NST, grid, PK);
     hipLaunchKernelGGL((gated_kernel<BM, BH, NST, MODE, PK>), dim3((unsigned)grid), dim3(512), 0, stream, k);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || !k.hq) return err;
     const int64_t blocks = (int64_t)p.rows_a * (p.I / 128);
     hipLaunchKernelGGL(gated_encode_kernel<PK>, dim3((unsigned)((blocks + 15) / 16)), dim3(256), 0, stream, k);
+    return hipGetLastError();
+}
+
+template <bool PK>
+static hipError_t launch_units(const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config) {
+    const GatedArgs k = args_of(p, 256, 128, num_cus);
+    // every expert's last unit may hold one block, and no unit holds less; the
+    // rest takes at most one workgroup per CU, half of them in place of units
+    const int64_t nblocks = p.rows_a / 128, most = nblocks / 2 + p.G + 1;
+    const int64_t grid = (most < nblocks ? most : nblocks) * k.tiles_n + num_cus;
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    describe(config, Mode::Contig, "tile=256x256x128 rest: tile=128x256x128", 2, grid, PK);
+    hipLaunchKernelGGL((gated_units_kernel<PK>), dim3((unsigned)grid), dim3(512), 0, stream, k);
     return hipGetLastError();
 }
 
@@ -560,13 +590,15 @@ static Tile choose_tile(int rows, int spare, int groups, int I, int K, bool narr
 
 template <Mode MODE, bool PK>
 static hipError_t launch_tile(Tile t, const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config) {
-    if (t.rows == 256) return launch_t<256, 128, 2, MODE, PK>(p, num_cus, kAllRows, stream, config);
+    if constexpr (MODE != Mode::Contig) {           // contiguous: launch_units
+        if (t.rows == 256) return launch_t<256, 128, 2, MODE, PK>(p, num_cus, stream, config);
+    }
     if (t.rows == 128)
-        return t.cols == 128 ? launch_t<128, 128, 3, MODE, PK>(p, num_cus, kAllRows, stream, config)
-                             : launch_t<128, 64, 3, MODE, PK>(p, num_cus, kAllRows, stream, config);
-    return t.cols == 128  ? launch_t<64, 128, 3, MODE, PK>(p, num_cus, kAllRows, stream, config)
-           : t.cols == 64 ? launch_t<64, 64, 3, MODE, PK>(p, num_cus, kAllRows, stream, config)
-                          : launch_t<64, 32, 3, MODE, PK>(p, num_cus, kAllRows, stream, config);
+        return t.cols == 128 ? launch_t<128, 128, 3, MODE, PK>(p, num_cus, stream, config)
+                             : launch_t<128, 64, 3, MODE, PK>(p, num_cus, stream, config);
+    return t.cols == 128  ? launch_t<64, 128, 3, MODE, PK>(p, num_cus, stream, config)
+           : t.cols == 64 ? launch_t<64, 64, 3, MODE, PK>(p, num_cus, stream, config)
+                          : launch_t<64, 32, 3, MODE, PK>(p, num_cus, stream, config);
 }
 
 // Dense: rows of the full rounds of 256x128 tiles.
@@ -586,7 +618,7 @@ static hipError_t launch_pk(const GatedProblem &p, int num_cus, hipStream_t stre
         if (head > 0) {
             GatedProblem q = p;
             q.rows_a = head;
-            const hipError_t err = launch_t<256, 128, 2, Mode::Dense, PK>(q, num_cus, kAllRows, stream, config);
+            const hipError_t err = launch_t<256, 128, 2, Mode::Dense, PK>(q, num_cus, stream, config);
             if (err != hipSuccess || rest == 0) return err;
         }
         GatedProblem q = p;
@@ -610,9 +642,7 @@ static hipError_t launch_pk(const GatedProblem &p, int num_cus, hipStream_t stre
         if (t.rows == 64 || t.cols < 128) return launch_tile<Mode::Contig, PK>(t, p, num_cus, stream, config);
         if (p.rows_a < 256 || (t.rows == 128 && p.rows_a / 128 * tiles_n <= num_cus))
             return launch_tile<Mode::Contig, PK>(kTiles[1], p, num_cus, stream, config);
-        const hipError_t err = launch_t<256, 128, 2, Mode::Contig, PK>(p, num_cus, kHead, stream, config);
-        if (err != hipSuccess) return err;
-        return launch_t<128, 128, 3, Mode::Contig, PK>(p, num_cus, kTail, stream, config);
+        return launch_units<PK>(p, num_cus, stream, config);
     }
     case Mode::Masked: {
         // the groups' counts are on the device: the caller's hint, or the capacity
