@@ -27,7 +27,7 @@ int rmsnorm_impl(const void *x, int x_type, int64_t ld_x, const void *residual, 
     if (!type_ok(x_type) || !type_ok(residual_type) || !type_ok(weight_type) || !(eps >= 0.0f)) return DG_ERR_ARG;
     if (rows > 0 && (!x || !weight || (!q && !y) || (q && !sf))) return DG_ERR_NULL;
     if (residual_out && !residual) return DG_ERR_ARG;
-    if (ld_x < K || ld_x * type_size(x_type) % 16 != 0) return DG_ERR_ALIGN;
+    if (ld_x < K || ld_x % (16 / type_size(x_type)) != 0) return DG_ERR_ALIGN;
     if (q && (ld_sf < rows || ld_sf % 4 != 0)) return DG_ERR_ALIGN;
     if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) || !aligned16(y) ||
         !aligned16(q) || !aligned16(sf))
@@ -105,15 +105,16 @@ int gated_contiguous(const uint8_t *a, const void *sfa, const uint8_t *b, const 
                      stream);
 }
 
-int gated_masked(const uint8_t *a, const void *sfa, const uint8_t *b, const void *sfb, int act, const GatedOut &o,
+int gated_masked(const uint8_t *a, const void *sfa, const uint8_t *b, const void *sfb, int act, GatedOut o,
                  const int32_t *masked_m, int G, int M_cap, int I, int K, int expected_m, void *stream, bool packed) {
-    if (G < 1 || M_cap < 1) return DG_ERR_SHAPE;
-    const int st = gated_check(a, sfa, b, sfb, act, o, M_cap, (M_cap + 3) / 4 * 4, I, K);
+    if (G < 1 || M_cap < 1 || M_cap > INT32_MAX - 3) return DG_ERR_SHAPE;
+    o.ld_sf = (M_cap + 3) / 4 * 4;                     // of sfa too
+    const int st = gated_check(a, sfa, b, sfb, act, o, M_cap, o.ld_sf, I, K);
     if (st != DG_OK) return st;
     if (!masked_m) return DG_ERR_NULL;
     if (!aligned4(masked_m)) return DG_ERR_ALIGN;
     return gated_run({a, static_cast<const float *>(sfa), b, static_cast<const float *>(sfb), masked_m, o.gu, o.h, o.q,
-                      o.sf, M_cap, I, K, (M_cap + 3) / 4 * 4, o.ld_sf, G, act, dg::Mode::Masked, expected_m, packed,
+                      o.sf, M_cap, I, K, o.ld_sf, o.ld_sf, G, act, dg::Mode::Masked, expected_m, packed,
                       nullptr, 0},
                      stream);
 }
@@ -233,7 +234,7 @@ int dg_m_grouped_fp8_gated_gemm_nt_masked(const uint8_t *a, const float *sfa, co
                                           int act, uint16_t *gu, uint16_t *h, uint8_t *q, float *sf,
                                           const int32_t *masked_m, int G, int M_cap, int I, int K, int expected_m,
                                           void *stream) {
-    return gated_masked(a, sfa, b, sfb, act, {gu, h, q, sf, (M_cap + 3) / 4 * 4}, masked_m, G, M_cap, I, K, expected_m,
+    return gated_masked(a, sfa, b, sfb, act, {gu, h, q, sf, 0}, masked_m, G, M_cap, I, K, expected_m,
                         stream, false);
 }
 
@@ -241,7 +242,7 @@ int dg_m_grouped_fp8_gated_gemm_nt_masked_ue8m0_packed(const uint8_t *a, const u
                                                        const uint32_t *sfb, int act, uint16_t *gu, uint16_t *h,
                                                        uint8_t *q, uint32_t *sf, const int32_t *masked_m, int G,
                                                        int M_cap, int I, int K, int expected_m, void *stream) {
-    return gated_masked(a, sfa, b, sfb, act, {gu, h, q, sf, (M_cap + 3) / 4 * 4}, masked_m, G, M_cap, I, K, expected_m,
+    return gated_masked(a, sfa, b, sfb, act, {gu, h, q, sf, 0}, masked_m, G, M_cap, I, K, expected_m,
                         stream, true);
 }
 
