@@ -3,7 +3,9 @@
 // 30 ns a tensor instead of 350 ns for the same checks in Python (a small
 // norm or decode call is otherwise bound by them).  It decides nothing by
 // itself: where a check fails, the binding repeats the checks in Python, which
-// name the argument and raise.
+// name the argument and raise.  So does an exception of torch's (a tensor
+// without storage, as under torch.vmap, has no address to give): none may
+// leave this C entry.
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -47,19 +49,27 @@ PyObject *addresses(PyObject *, PyObject *const *args, Py_ssize_t n) {
                 Py_DECREF(out);
                 return nullptr;
             }
-            bool ok = v.defined() && v.layout() == at::kStrided && v.is_cuda() && v.get_device() == device &&
-                      (type_bit(v.scalar_type()) & mask) != 0 && v.dim() == PyTuple_GET_SIZE(shape) && v.is_contiguous();
-            for (Py_ssize_t d = 0; ok && d < v.dim(); ++d) {
-                const long want = PyLong_AsLong(PyTuple_GET_ITEM(shape, d));
-                if (want == -1 && PyErr_Occurred()) {
-                    Py_DECREF(out);
-                    return nullptr;
+            bool ok = false;
+            void *data = nullptr;
+            try {
+                ok = v.defined() && v.layout() == at::kStrided && v.is_cuda() && v.get_device() == device &&
+                     (type_bit(v.scalar_type()) & mask) != 0 && v.dim() == PyTuple_GET_SIZE(shape) && v.is_contiguous();
+                for (Py_ssize_t d = 0; ok && d < v.dim(); ++d) {
+                    const long want = PyLong_AsLong(PyTuple_GET_ITEM(shape, d));
+                    if (want == -1 && PyErr_Occurred()) {
+                        Py_DECREF(out);
+                        return nullptr;
+                    }
+                    ok = v.size(d) == want;
                 }
-                ok = v.size(d) == want;
+                // an empty tensor has no address: NULL, as the library takes it
+                if (ok && v.numel()) data = v.data_ptr();
+            } catch (...) {
+                PyErr_Clear();
+                ok = false;
             }
             if (ok) {
-                // an empty tensor has no address: NULL, as the library takes it
-                value = PyLong_FromVoidPtr(v.numel() ? v.data_ptr() : nullptr);
+                value = PyLong_FromVoidPtr(data);
                 if (!value) {
                     Py_DECREF(out);
                     return nullptr;
