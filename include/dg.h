@@ -546,7 +546,8 @@ int64_t dg_get_gated_workspace_size(int M, int I, int K);
  * Its M-grouped forms, with the row layouts of the plain M-grouped GEMMs: b
  * [G][2][I][K], sfb [G][2][ceil(I/128)][K/128].
  * Contiguous: a, gu, h, q of M_total rows (a multiple of 128), sfa
- * [K/128][M_total], sf [I/128][M_total], m_indices [M_total] (16-byte aligned).
+ * [K/128][M_total], sf [I/128][M_total], m_indices [M_total] (16-byte aligned);
+ * the experts' 128-row blocks may come in any order.
  * Masked: a [G][M_cap][K], sfa [G][K/128][round_up(M_cap,4)], outputs
  * [G][M_cap][..], sf [G][I/128][round_up(M_cap,4)], masked_m [G] on the device.
  * Rows that hold no data are not written, in any output, sf included.
