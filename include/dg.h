@@ -185,7 +185,8 @@ int dg_fp8_gemm_tt(const uint8_t *a, const float *sfa, int ld_sfa,
  *             a 128-row block whose first id lies outside [0, G) is treated
  *             as padding too (so a bad id never reads outside b and sfb).
  * Precondition (not checked on the device): each aligned 128-row block holds
- * rows of at most one expert, valid rows first.
+ * rows of at most one expert, valid rows first.  The blocks may come in any
+ * order (an expert may own several segments).
  * Errors: DG_ERR_NULL, DG_ERR_SHAPE (M_total % 128, N, K, G < 1), DG_ERR_ALIGN.
  */
 int dg_m_grouped_fp8_gemm_nt_contiguous(const uint8_t *a, const float *sfa,

@@ -238,6 +238,10 @@ pipe_kernel(PipeParams p) {
     if (SPLIT) {
         tm = t_lin / p.tiles_n;
         tn = t_lin % p.tiles_n;
+    } else if (MODE == Mode::Contig && BM == 256 && (int)blockIdx.x >= total) {
+        // units past those that one segment per expert makes
+        raster((int)blockIdx.x - total, p.rows_a / 128 - p.tiles_m, p.tiles_n, p.gm, tm, tn);
+        tm += p.tiles_m;
     } else {
         raster(t_lin, p.tiles_m, p.tiles_n, p.gm, tm, tn);
     }
@@ -797,6 +801,9 @@ bool pipe_eligible(const GemmProblem &p) {
     return (int64_t)p.rows_a * p.K < lim && (int64_t)p.N * p.K < lim && p.ld_sfa >= 1;
 }
 
+// Contiguous layout: 256-row units that one segment per expert makes at most.
+static int usual_units(const GemmProblem &p) { return p.rows_a / 256 + p.G + 1; }
+
 // Launches pipe_kernel.  With SPLIT, `units` is the number of workgroups to
 // aim for: when it exceeds the number of tiles, the K steps of each tile are
 // split over about units/tiles workgroups (some tiles one more than others,
@@ -814,9 +821,10 @@ hipError_t launch_pipe_t(const GemmProblem &p, int units, hipStream_t stream, st
     k.d32 = p.d32;
     k.tiles_m = (p.rows_a + BM - 1) / BM;
     if (MODE == Mode::Contig && BM == 256) {
-        // units: at most one per 256 rows plus one per expert segment
+        // units: at most one per 256 rows plus one per expert segment, of
+        // which an expert usually has one (other orders: below)
         if (p.rows_a % 128 != 0) return hipErrorInvalidValue;
-        k.tiles_m = p.rows_a / 256 + p.G + 1;
+        k.tiles_m = usual_units(p);
     }
     k.tiles_n = (p.N + BN - 1) / BN;
     k.gm = 4;
@@ -850,6 +858,11 @@ hipError_t launch_pipe_t(const GemmProblem &p, int units, hipStream_t stream, st
             split = true;
         }
     }
+    if (MODE == Mode::Contig && BM == 256 && p.rows_a / 128 > k.tiles_m)
+        // the experts' blocks may come in any order, with up to one unit per
+        // block; these workgroups come last and end at once where there are
+        // fewer units
+        grid += (int64_t)(p.rows_a / 128 - k.tiles_m) * k.tiles_n;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     char buf[220];
     snprintf(buf, sizeof buf,
@@ -904,13 +917,21 @@ static hipError_t launch_pipe_ue(const GemmProblem &p, int num_cus, hipStream_t 
             return launch_pipe_t<256, 256, 2, 4, 2, 1, true, Mode::Dense, false, UE, false, false, PK>(p, 0, stream, config);
         return launch_pipe_t<128, 128, 2, 4, 2, 1, true, Mode::Dense, false, UE, false, false, PK>(p, 0, stream, config);
     }
-    case Mode::Contig:
+    case Mode::Contig: {
         // 256-row units that never mix experts (the segments are 128-row
         // aligned); measured on MI355X for 8 experts, N = 4096, K = 7168:
-        // 540 us against 575 us with 128x256 tiles
-        if (p.rows_a >= 256)
+        // 540 us against 575 us with 128x256 tiles.  The workgroups that wait
+        // for units of experts with several segments take some 4 us per round
+        // of the CUs to find none, which shows with a short K only (16 experts,
+        // 1024 blocks, N = 512: K = 512 118 against 99 us without them, K = 2304
+        // 222 and 223); there the smaller tiles, one per block and free of the
+        // walk, are faster than either (67 us; 8 experts, 256 blocks, N = 2048,
+        // K = 2048: 157 against 167)
+        const int64_t waiting = (int64_t)(p.rows_a / 128 - usual_units(p)) * ((p.N + 255) / 256);
+        if (p.rows_a >= 256 && (waiting <= cus || p.K > 2048))
             return launch_pipe_t<256, 256, 2, 4, 2, 1, true, Mode::Contig, false, UE, false, false, PK>(p, 0, stream, config);
         return launch_pipe_t<128, 256, 2, 4, 3, 1, true, Mode::Contig, false, UE, false, false, PK>(p, 0, stream, config);
+    }
     case Mode::Masked:
         return launch_pipe_t<128, 256, 2, 4, 3, 1, true, Mode::Masked, false, UE, false, false, PK>(p, 0, stream, config);
     case Mode::KGrouped: break;                    // launched by launch_pipe
