@@ -135,12 +135,30 @@ rmsnorm_quant_kernel(NormFwdArgs p) {
     });
 }
 
+// A grid of 2^32 threads or more is not refused but taken modulo 2^32: more
+// rows than a grid holds go in several launches.
 template <typename TX, typename TR, typename TW, int WPR, int NCH>
 static hipError_t launch_fwd_t(const NormFwdArgs &a, hipStream_t stream) {
-    const int64_t grid = WPR == 1 ? ((int64_t)a.rows + 3) / 4 : a.rows;
-    hipLaunchKernelGGL((rmsnorm_quant_kernel<TX, TR, TW, WPR, NCH>), dim3((unsigned)grid),
-                       dim3(WPR == 1 ? 256 : 64 * WPR), 0, stream, a);
-    return hipGetLastError();
+    constexpr int kThreads = WPR == 1 ? 256 : 64 * WPR, kRows = WPR == 1 ? 4 : 1;      // of a workgroup
+    constexpr int64_t kMost = ((int64_t)1 << 32) / kThreads / 2 * kRows;               // rows of a launch
+    using TRS = typename std::conditional<std::is_same<TR, NoRes>::value, TX, TR>::type;
+    for (int64_t r = 0; r < a.rows; r += kMost) {
+        NormFwdArgs p = a;
+        p.rows = (int)(a.rows - r < kMost ? a.rows - r : kMost);
+        p.x = static_cast<const TX *>(a.x) + r * a.ld_x;
+        if (a.res) p.res = static_cast<const TRS *>(a.res) + r * a.K;
+        if (a.res_out) p.res_out = static_cast<TRS *>(a.res_out) + r * a.K;
+        if (a.y) p.y = a.y + r * a.K;
+        if (a.q) {
+            p.q = a.q + r * a.K;
+            p.sf = static_cast<float *>(a.sf) + r;
+        }
+        hipLaunchKernelGGL((rmsnorm_quant_kernel<TX, TR, TW, WPR, NCH>), dim3((unsigned)((p.rows + kRows - 1) / kRows)),
+                           dim3(kThreads), 0, stream, p);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 // Waves per row: one up to 1024 columns (16384 rows: 14 against 25 us with
