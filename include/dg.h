@@ -27,7 +27,8 @@
  *  - Calls are asynchronous on `stream` (a hipStream_t; NULL = the default
  *    stream).  Argument errors are detected on the host and returned before
  *    anything is launched; nothing is written then.  A failed launch returns
- *    DG_ERR_HIP.  Device faults surface at the caller's next synchronisation.
+ *    DG_ERR_HIP, and so do sizes that would take a grid of 2^32 threads (some
+ *    10^6 to 10^7 workgroups).  Device faults surface at the caller's next synchronisation.
  *  - D is bf16, rounded to nearest even from the fp32 accumulator.  C is bf16
  *    of the same shape as D, or NULL for C = 0; C may alias D exactly.
  *  - K must be a positive multiple of 128.  M and N may be any positive size

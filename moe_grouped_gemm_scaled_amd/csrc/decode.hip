@@ -389,7 +389,7 @@ static hipError_t launch_skinny_t(const GemmProblem &p, int splits, hipStream_t 
     }
     k.splits = splits;
     const int64_t grid = tiles * splits;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (!grid_fits(grid, NT)) return hipErrorInvalidValue;
     char buf[200];
     snprintf(buf, sizeof buf, "family=skinny mode=%d rows=%d cols=%d waves=%dx%d ks=%d pd=%d splits=%d grid=%lld",
              (int)MODE, ROWS, BN, WGM, WGN, KS, PD, splits, (long long)grid);

@@ -16,6 +16,10 @@ namespace dg {
 // 4q + j (0 past the last K block).
 hipError_t launch_pack_ue8m0(const float *sf, int outer, int kblocks, int inner, uint32_t *out, hipStream_t stream);
 
+// Whether a launch of this many workgroups is what it says: HIP takes a grid of
+// 2^32 threads or more modulo 2^32, without an error.
+inline bool grid_fits(int64_t groups, int threads) { return groups <= (((int64_t)1 << 32) - 1) / threads; }
+
 // ue8m0: the block scale rounded up to a power of two
 hipError_t launch_quant_1x128(const float *x, int groups, int rows, int K, uint8_t *q, float *sf,
                               int ld_sf, hipStream_t stream, bool ue8m0);

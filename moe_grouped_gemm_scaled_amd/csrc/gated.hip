@@ -558,7 +558,7 @@ template <int BM, int BH, int NST, Mode MODE, bool PK>
 static hipError_t launch_t(const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config) {
     const GatedArgs k = args_of(p, BM, BH, num_cus);
     const int64_t grid = (int64_t)k.tiles_m * k.tiles_n * (MODE == Mode::Masked ? p.G : 1);
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (!grid_fits(grid, 512)) return hipErrorInvalidValue;
     char tile[32];
     snprintf(tile, sizeof tile, "tile=%dx%dx128", BM, 2 * BH);
     describe(config, MODE, tile, NST, grid, PK);
@@ -580,7 +580,7 @@ static hipError_t launch_units(const GatedProblem &p, int num_cus, hipStream_t s
     const int64_t first = (most < nblocks ? most : nblocks) * k.tiles_n + num_cus / 2;
     const int64_t more = nblocks * k.tiles_n + num_cus / 2 - first;
     const int64_t grid = first + (more < num_cus ? more : num_cus);
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (!grid_fits(grid, 512)) return hipErrorInvalidValue;
     describe(config, Mode::Contig, "tile=256x256x128 rest: tile=128x256x128", 2, grid, PK);
     hipLaunchKernelGGL((gated_units_kernel<PK>), dim3((unsigned)grid), dim3(512), 0, stream, k, (int)first);
     return hipGetLastError();
@@ -602,13 +602,16 @@ constexpr Tile kTiles[] = {{256, 128, 100}, {128, 128, 60}, {128, 64, 38}, {64, 
 constexpr int kRoundCost = 150, kEncodeCost = 300;
 
 // narrow: tiles of fewer than 128 columns can serve.  encode: they need the
-// second kernel.  spare: rows that 256-row tiles waste besides.
-static Tile choose_tile(int rows, int spare, int groups, int I, int K, bool narrow, bool encode, int num_cus) {
+// second kernel.  spare: rows that 256-row tiles waste besides.  cap: rows that
+// are launched, of which `rows` are expected to hold data.
+static Tile choose_tile(int rows, int cap, int spare, int groups, int I, int K, bool narrow, bool encode, int num_cus) {
     Tile best = kTiles[0];
     int64_t least = INT64_MAX;
     for (const Tile &t : kTiles) {
         if (t.cols < 128 && !narrow) continue;
         const int64_t tiles = groups * ((rows + (t.rows == 256 ? (int64_t)spare : 0) + t.rows - 1) / t.rows) * ((I + t.cols - 1) / t.cols);
+        // many groups of few columns: a larger tile
+        if (!grid_fits(groups * (((int64_t)cap + t.rows - 1) / t.rows) * ((I + t.cols - 1) / t.cols), 512)) continue;
         const int64_t c = (tiles + num_cus - 1) / num_cus * ((int64_t)t.cost * (K / kKBlock) + kRoundCost) +
                           (t.cols < 128 && encode ? kEncodeCost : 0);
         if (c < least) {
@@ -664,12 +667,12 @@ static hipError_t launch_pk(const GatedProblem &p, int num_cus, hipStream_t stre
             q.sf = static_cast<uint32_t *>(p.sf) + head;
         }
         const bool scratch = p.ws && p.ws_bytes >= (size_t)rest * p.I * sizeof(float);
-        const Tile t = choose_tile(rest, 0, 1, p.I, p.K, !p.q || scratch, p.q != nullptr, num_cus);
+        const Tile t = choose_tile(rest, rest, 0, 1, p.I, p.K, !p.q || scratch, p.q != nullptr, num_cus);
         return launch_tile<Mode::Dense, PK>(t, q, num_cus, stream, config);
     }
     case Mode::Contig: {
         // every expert's last unit may hold one block only: one more 256-row tile each
-        const Tile t = choose_tile(p.rows_a, 128 * p.G, 1, p.I, p.K, !p.q, false, num_cus);
+        const Tile t = choose_tile(p.rows_a, p.rows_a, 128 * p.G, 1, p.I, p.K, !p.q, false, num_cus);
         if (t.rows == 64 || t.cols < 128) return launch_tile<Mode::Contig, PK>(t, p, num_cus, stream, config);
         if (p.rows_a < 256 || (t.rows == 128 && p.rows_a / 128 * tiles_n <= num_cus))
             return launch_tile<Mode::Contig, PK>(kTiles[1], p, num_cus, stream, config);
@@ -678,7 +681,7 @@ static hipError_t launch_pk(const GatedProblem &p, int num_cus, hipStream_t stre
     case Mode::Masked: {
         // the groups' counts are on the device: the caller's hint, or the capacity
         const int expect = p.expected_m > 0 && p.expected_m < p.rows_a ? p.expected_m : p.rows_a;
-        const Tile t = choose_tile(expect, 0, p.G, p.I, p.K, !p.q, false, num_cus);
+        const Tile t = choose_tile(expect, p.rows_a, 0, p.G, p.I, p.K, !p.q, false, num_cus);
         return launch_tile<Mode::Masked, PK>(t, p, num_cus, stream, config);
     }
     case Mode::KGrouped: break;
@@ -690,7 +693,7 @@ size_t gated_workspace(int M, int I, int K, int num_cus) {
     if (M <= kGatedSmallMaxM) return gated_small_workspace(M, I, K, num_cus);
     if (I % 128 != 0) return 0;                    // no quantised output
     const int rest = M - head_rows(M, I, num_cus);
-    return rest > 0 && choose_tile(rest, 0, 1, I, K, true, true, num_cus).cols < 128 ? (size_t)rest * I * sizeof(float) : 0;
+    return rest > 0 && choose_tile(rest, rest, 0, 1, I, K, true, true, num_cus).cols < 128 ? (size_t)rest * I * sizeof(float) : 0;
 }
 
 hipError_t launch_gated(const GatedProblem &p, int num_cus, hipStream_t stream, std::string &config) {

@@ -230,7 +230,7 @@ static hipError_t launch_t(const GatedBwdArgs &a, int64_t tiles, int num_cus, hi
 hipError_t launch_gated_bwd(const GatedBwdProblem &p, int num_cus, hipStream_t stream) {
     const int tiles_n = p.I / 128;
     const int64_t grid = ((int64_t)p.rows + 127) / 128 * tiles_n;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (!grid_fits(grid, 512)) return hipErrorInvalidValue;
     const GatedBwdArgs a{p.gu, p.dh, p.idx, p.dgu, p.q, p.sf, p.qt, p.sft, p.ht, p.sfht, p.rows, p.I, p.ld_sf, tiles_n};
     if (p.act == kActSilu)
         return p.ue8m0 ? launch_t<kActSilu, true>(a, grid, num_cus, stream)

@@ -262,7 +262,7 @@ static hipError_t launch_tiled(const GemmProblem &p, hipStream_t stream, std::st
     k.gm = 8;
     const int64_t groups = MODE == Mode::Masked ? p.G : 1;
     const int64_t grid = (int64_t)k.tiles_m * k.tiles_n * groups;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (!grid_fits(grid, 64 * WM * WN)) return hipErrorInvalidValue;
     char buf[160];
     snprintf(buf, sizeof buf, "family=tiled mode=%d tile=%dx%dx128 waves=%dx%d grid=%lld", (int)MODE, BM, BN, WM,
              WN, (long long)grid);

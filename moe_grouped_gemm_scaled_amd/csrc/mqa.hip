@@ -298,7 +298,7 @@ hipError_t launch_nt(const MqaParams &p, hipStream_t stream, std::string &config
     k.n_qblk = (p.S + 4 * NQ - 1) / (4 * NQ);
     k.n_chunk = (p.Skv + CH_STAGES * kStageKeys - 1) / (CH_STAGES * kStageKeys);
     const long grid = (long)((k.n_qblk + 7) / 8) * 8 * k.n_chunk;
-    if (grid > 0x7fffffffL) return hipErrorInvalidValue;
+    if (!grid_fits(grid, 256)) return hipErrorInvalidValue;
     char buf[160];
     snprintf(buf, sizeof buf, "family=mqa heads=%d queries/wg=%d chunk=%d stages=%d grid=%ld%s", 16 * NT, 4 * NQ,
              CH_STAGES * kStageKeys, NST, grid, k.vec ? "" : " scalar-stores");

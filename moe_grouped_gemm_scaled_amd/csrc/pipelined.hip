@@ -863,7 +863,7 @@ hipError_t launch_pipe_t(const GemmProblem &p, int units, hipStream_t stream, st
         // block; these workgroups come last and end at once where there are
         // fewer units
         grid += (int64_t)(p.rows_a / 128 - k.tiles_m) * k.tiles_n;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (!grid_fits(grid, 64 * WGM * WGN)) return hipErrorInvalidValue;
     char buf[220];
     snprintf(buf, sizeof buf,
              "family=pipe mode=%d tile=%dx%dx128 waves=%dx%d stages=%d kblocks_per_stage=%d deep=%d splits=%d%s "

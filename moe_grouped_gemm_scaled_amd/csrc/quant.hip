@@ -141,7 +141,7 @@ hipError_t launch_pack_ue8m0(const float *sf, int outer, int kblocks, int inner,
     const int words = (kblocks + 3) / 4;
     const int64_t total = (int64_t)outer * words * inner;
     const int64_t grid = (total + 255) / 256;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (!grid_fits(grid, 256)) return hipErrorInvalidValue;
     hipLaunchKernelGGL(pack_ue8m0_kernel, dim3((unsigned)grid), dim3(256), 0, stream, sf, kblocks, inner, words, out,
                        total);
     return hipGetLastError();
@@ -153,7 +153,7 @@ static hipError_t launch_quant_1x128_u(const float *x, int groups, int rows, int
     const int64_t rows_total = (int64_t)groups * rows;
     const int kb_tiles = (nkb + 4 * U - 1) / (4 * U);        // runs of 4U K blocks per workgroup
     const int64_t grid = (rows_total + 7) / 8 * kb_tiles;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (!grid_fits(grid, 256)) return hipErrorInvalidValue;
     if (ue8m0)
         hipLaunchKernelGGL((quant_1x128_kernel<true, U>), dim3((unsigned)grid), dim3(256), 0, stream,
                            x, q, sf, rows, nkb, ld_sf, rows_total, kb_tiles);
@@ -179,7 +179,7 @@ hipError_t launch_quant_128x128(const float *x, int groups, int rows, int K, uin
     const int nkb = K / kKBlock;
     const int nrb = (rows + 127) / 128;
     const int64_t grid = (int64_t)groups * nrb * nkb;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (!grid_fits(grid, 256)) return hipErrorInvalidValue;
     if (ue8m0)
         hipLaunchKernelGGL(quant_128x128_kernel<true>, dim3((unsigned)grid), dim3(256), 0, stream,
                            x, q, sf, rows, K, nrb, nkb);

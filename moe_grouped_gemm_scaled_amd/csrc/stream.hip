@@ -401,7 +401,7 @@ static hipError_t launch_stream_t(const GemmProblem &p, int units, hipStream_t s
             split = true;
         }
     }
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (!grid_fits(grid, 64 * WGM * WGN)) return hipErrorInvalidValue;
     char buf[200];
     snprintf(buf, sizeof buf, "family=stream rows=%d cols=%d waves=%dx%d stages=%d splits=%d%s grid=%lld", ROWS, BN,
              WGM, WGN, NST, split ? k.splits_lo : 1, split && k.split_hi > 0 ? "+" : "", (long long)grid);
