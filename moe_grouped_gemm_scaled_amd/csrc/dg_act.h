@@ -3,6 +3,8 @@
 // form of GELU, 0.5 g (1 + tanh z) with z = sqrt(2/pi) (g + 0.044715 g^3), has
 // v = 2z, since (1 + tanh z) / 2 = s(2z).  So
 //     act'(g) = s + act(g) (1 - s) v'.
+// act(g) (1 - s) is 0 long before g^2 in GELU's v' leaves the range of fp32; the
+// square is bounded there, so that the product stays 0.
 // s(v) = 1 / (1 + 2^(-v log2 e)) with the hardware exponential and reciprocal
 // (about 1 ulp each), without cancellation for any v; v -> -inf gives 0.
 #pragma once
@@ -30,7 +32,7 @@ __device__ __forceinline__ void act_and_grad(float g, float &a, float &da) {
     const float s = act_sigmoid<ACT>(g);
     a = g * s;
     float k = 1.0f;
-    if constexpr (ACT == kActGelu) k = __builtin_fmaf(0.21406445f, g * g, 1.5957691f);
+    if constexpr (ACT == kActGelu) k = __builtin_fmaf(0.21406445f, fminf(g * g, 1e30f), 1.5957691f);
     da = __builtin_fmaf(a * (1.0f - s), k, s);
 }
 
