@@ -50,12 +50,14 @@ __device__ __forceinline__ float block_scale(float amax) {
 }
 
 // Division by a block's scale in fp32 only, for kernels whose arithmetic shows
-// beside their memory time: x / s rounded to fp32 as
-//     q0 = RN(x y),  e = q0 s - x,  q = RN(q0 - e y)   with y = RN(1 / s).
-// e is exact (one fma), and then q is the IEEE quotient (Markstein, "Computation
-// of elementary functions on the IBM RISC System/6000 processor", 1990): y is
-// correctly rounded and q0 within an ulp of the quotient.  Subnormal
-// intermediates may break that only for quotients that encode as zero.
+// beside their memory time: with y = RN(1 / s),
+//     q0 = RN(x y),  e = RN(q0 s - x),  q = RN(q0 - e y)      (each line one rounding)
+// q0 is within 1.5 ulp of z = x / s, and the relative errors of y and e, 2^-24
+// each, leave what the last step rounds within 1.5 * 2^-23 ulp of z.  So q is
+// the IEEE quotient or, next to a midpoint of fp32, its neighbour, which gives
+// another E4M3 code only where one of the two is a boundary between codes.  The
+// pairs x, s of 24 bits that come so close to a midpoint beside a boundary are
+// few; all of them give the code of the IEEE quotient (tests).
 // In this form e = +0 for x = +-0 leaves the sign of the zero.  Power-of-two
 // scales: x y is exact.  An infinite scale (y = 0) counts as 0 in e, which keeps
 // 0 for finite x and NaN for infinities.

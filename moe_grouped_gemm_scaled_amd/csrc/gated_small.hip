@@ -17,7 +17,7 @@
 // columns and so read A less often; and a quantised output needs a row's
 // maximum over 128 columns, which no workgroup has.  In both cases the sums
 // go to the caller's workspace in fp32, and a second kernel adds the S partial
-// sums in order and finishes h: one wave per 16 (row, 128-column) blocks.  (A
+// sums in order and finishes h: one wave per 4 (row, 128-column) blocks.  (A
 // single kernel whose last workgroup finishes a block, behind device-coherent
 // stores and a counter, took about 1 us longer per call and needed the
 // workspace zeroed.)
