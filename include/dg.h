@@ -414,8 +414,12 @@ int dg_fp8_mqa_logits(const uint8_t *q, const uint8_t *kv, const float *kv_scale
  *   d   [G][M][N]     fp32, written entirely.
  * Accumulation as in dg_fp8_gemm_nt (fp32, one promotion per 128-row K
  * block), so D meets the GEMMs' bar without their final bf16 rounding:
- * |D - D_ref| <= 2^-20 |D_ref| + 1e-4 max|D_ref|.  Needs M and N multiples
- * of 16, K*M and K*N below 2^31.
+ * |D - D_ref| <= 2^-20 |D_ref| + 1e-4 max|D_ref|, where many products of like
+ * size make a result.  The FP8 instruction keeps 13 bits below the largest of
+ * eight consecutive products, which is up to 2^-12 of the sum of the products'
+ * magnitudes: with one or two K blocks and operands of a few large values
+ * (gradients) that alone may pass 1e-4 max|D_ref|.  Needs M and N multiples of
+ * 16, K*M and K*N below 2^31.
  * Errors: DG_ERR_NULL (a, sfa, b, sfb, ks, d), DG_ERR_SHAPE (M, N, G < 1;
  * K < 128 or K % 128; K*M or K*N too large), DG_ERR_ALIGN (M or N not a
  * multiple of 16; a, sfa, b, sfb, c, d not 16-B aligned; ks not 4-B aligned).

@@ -6,8 +6,11 @@
 // same columns), all rows of A, and all of K, which is split over its waves.
 // Each wave streams its K blocks (16 B rows and all A rows of the block)
 // through a ring of NST LDS stages of its own, filled by DMA, so no barrier
-// stands in the K loop, I / 8 workgroups spread B over the CUs, and about
-// 150 KB per CU are in flight.  A is read by every workgroup, from L2.  Loading
+// stands in the K loop, and I / 8 workgroups (or half as many) spread B over the
+// CUs.  The rings of a workgroup hold 65 to 80 KB up to 64 rows, so about 150 KB
+// per CU where the grid gives every CU two workgroups, and half of that where it
+// gives one (I = 2048); above 64 rows 127 to 154 KB.  A is read by every
+// workgroup, from L2.  Loading
 // fragments straight into registers needs no LDS, but 16 lanes then touch 16
 // rows: 33 KB/us per CU against 80 to 100 with 8 lanes on each 128-byte line
 // (measured on L2-resident data), 20.8 against 10.9 us at 64 rows, I = 2048,
