@@ -463,8 +463,12 @@ def _run_own(s):
                                              scales=_SCALES[c["scales"]])
     else:
         cols = {k: s[k] for k in ("src", "qt", "sft") if c["cols"]}
-        dg.moe_dispatch_quantize_e4m3_contiguous(s["x"], s["rows"], s["R"], q=s["q"], sf=s["sf"],
-                                                 scales=_SCALES[c["scales"]], **cols)
+        rows = {"q": s["q"], "sf": s["sf"]}
+        if c["cols"] and c["scales"] == "packed":       # a call has one scale format; the weight gradient's is fp32 here
+            dg.moe_dispatch_quantize_e4m3_contiguous(s["x"], s["rows"], s["R"], scales="ue8m0_packed", **rows)
+            rows = {}
+        scales = _SCALES[c["scales"]] if rows else "fp32"
+        dg.moe_dispatch_quantize_e4m3_contiguous(s["x"], s["rows"], s["R"], scales=scales, **rows, **cols)
     out = {k: s[k] for k in ("rows", "src", "masked_m", "m_indices", "ks", "sft") if k in s}
     out.update({k: s[k].view(E4M3) for k in ("q", "qt") if k in s})
     out["sf"] = _sf_value(c["scales"], s["sf"])
