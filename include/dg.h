@@ -3,7 +3,8 @@
  * NT GEMM and its M-grouped MoE forms, the E4M3 quantisers, the NN/TN/TT
  * layouts, the K-grouped weight-gradient GEMM, power-of-two (UE8M0) scale
  * variants, the FP8 MQA logits, and the operators around the GEMMs of a
- * gated feed-forward layer (norm, gating and their gradients).
+ * gated feed-forward layer (norms, gating, the tokens' way to the experts'
+ * rows and back, and their gradients).
  *
  * Operation (the "DeepGEMM" README summary on GeekNews, ja.news.hada.io topic
  * 19459, section "GEMM interface and layout constraints"): D = C + A . B^T in
@@ -610,6 +611,210 @@ int dg_gated_backward_quantize_e4m3_ue8m0(const uint16_t *gu, const uint16_t *dh
                                           uint16_t *dgu, uint8_t *q, float *sf, int ld_sf,
                                           uint8_t *qt, float *sft, uint8_t *ht, float *sfht,
                                           int rows, int I, void *stream);
+
+/*
+ * Layer norm: the RMS norm's calls with the mean taken out and a bias,
+ *   h = x + residual;  m = mean_k(h);  v = mean_k((h - m)^2)
+ *   y = (h - m) / sqrt(v + eps) * weight + bias
+ *   q, sf = the 1x128 quantiser's output on y (before any rounding of y)
+ * Arguments as for dg_rmsnorm_quantize_e4m3_1x128, and
+ *   weight, bias [K]   each optional (NULL: ones, zeros), of one type
+ *   K                  a multiple of 128 where q is asked for, of 8 otherwise;
+ *                      8 to 16384
+ * The mean is subtracted before the squares are summed, so a mean that is large
+ * beside the spread costs no more bits than h itself holds.
+ * Errors as there.
+ */
+int dg_layernorm_quantize_e4m3_1x128(const void *x, int x_type, int64_t ld_x,
+                                     const void *residual, int residual_type,
+                                     const void *weight, const void *bias, int weight_type, float eps,
+                                     void *residual_out, uint16_t *y,
+                                     uint8_t *q, float *sf, int ld_sf,
+                                     int rows, int K, void *stream);
+int dg_layernorm_quantize_e4m3_1x128_ue8m0(const void *x, int x_type, int64_t ld_x,
+                                           const void *residual, int residual_type,
+                                           const void *weight, const void *bias, int weight_type, float eps,
+                                           void *residual_out, uint16_t *y,
+                                           uint8_t *q, float *sf, int ld_sf,
+                                           int rows, int K, void *stream);
+int dg_layernorm_quantize_e4m3_1x128_ue8m0_packed(const void *x, int x_type, int64_t ld_x,
+                                                  const void *residual, int residual_type,
+                                                  const void *weight, const void *bias, int weight_type, float eps,
+                                                  void *residual_out, uint16_t *y,
+                                                  uint8_t *q, uint32_t *sf, int ld_sf,
+                                                  int rows, int K, void *stream);
+
+/*
+ * Gradient of the layer norm, from its input h as stored (residual_out, or x
+ * where there is no residual); the quantisation is taken as the identity.
+ *   r = 1 / sqrt(v + eps),  n = (h - m) * r,  g = dy * weight
+ *   dx = dres + r * (g - mean_k(g) - n * mean_k(g * n))   [rows][K], h's type
+ *   dw = sum over rows of dy * n,  db = sum over rows of dy   [K] fp32, each optional
+ * weight, dres optional; the rest as for dg_rmsnorm_backward, K a multiple of 8.
+ *   workspace: dg_get_layernorm_backward_workspace_size(rows, K) bytes of
+ *   device memory, 16-byte aligned (NULL when that is 0, or neither dw nor db
+ *   is asked for), of any content.
+ */
+int dg_layernorm_backward(const void *dy, int dy_type, const void *h, int h_type,
+                          const void *weight, int weight_type, float eps,
+                          const void *dres, void *dx, float *dw, float *db, int rows, int K,
+                          void *workspace, size_t workspace_bytes, void *stream);
+int64_t dg_get_layernorm_backward_workspace_size(int rows, int K);
+
+/* ------------------------------------------------------------------------
+ * Tokens to the experts' rows and back.  T tokens choose top_k of G experts
+ * each; pair t * top_k + j is token t's choice j.  A pair whose id lies outside
+ * [0, G) (an expert that lives elsewhere, a token that was dropped) has no row:
+ * its entry of `rows` is -1, it is neither dispatched nor combined, and its
+ * weight's gradient is 0.  Index arrays are int32, 4-byte aligned; weights are
+ * fp32, 4-byte aligned.  Every result is computed in a fixed order: the same
+ * bits on every run.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * The sort: a row for every pair, in pair order within an expert.
+ *   ids  [T][top_k]   in device memory; an expert may occur twice in a token
+ *   rows [T][top_k]   the pair's row, -1 where it has none
+ * Contiguous: expert e's segment starts at the sum of the sizes before it, each
+ * rounded up to 128 rows.
+ *   m_indices [M_total]   optional, 16-byte aligned: the expert of each row, -1
+ *                         on rows that hold no pair
+ *   src       [M_total]   optional: the pair of each row, -1 likewise
+ *   counts    [G]         optional: rows that hold a pair
+ *   ks        [G]         optional: rows of the segment (a multiple of 128): the
+ *                         group sizes of the K-grouped GEMM
+ *   M_total   a multiple of 128.  dg_get_moe_rows(T, top_k, G) rows hold the
+ *             pairs however they fall; with fewer, pairs whose row would lie at
+ *             or past M_total have none.
+ * Masked: expert e's rows are e * M_cap onwards; pairs past M_cap have no row.
+ *   masked_m [G]          rows that hold a pair
+ *   src      [G][M_cap]   optional
+ *   workspace: dg_get_moe_sort_workspace_size(T, top_k, G) bytes of device
+ *   memory, 16-byte aligned, of any content; with NULL or too few bytes the
+ *   same results take longer where that is not 0.
+ * A call with T = 0 writes the plan of no pairs.
+ * Errors: DG_ERR_NULL (ids, rows with T > 0; masked_m); DG_ERR_SHAPE (T < 0,
+ * top_k < 1, G < 1 or > 1024, M_total < 0 or % 128, M_cap < 1; T * top_k + 128 G
+ * or the rows reaching 2^31); DG_ERR_ALIGN.
+ */
+int dg_moe_sort_contiguous(const int32_t *ids, int T, int top_k, int G,
+                           int32_t *rows, int32_t *src, int32_t *m_indices, int32_t *counts, int32_t *ks,
+                           int M_total, void *workspace, size_t workspace_bytes, void *stream);
+int dg_moe_sort_masked(const int32_t *ids, int T, int top_k, int G,
+                       int32_t *rows, int32_t *src, int32_t *masked_m,
+                       int M_cap, void *workspace, size_t workspace_bytes, void *stream);
+int64_t dg_get_moe_rows(int T, int top_k, int G);
+int64_t dg_get_moe_sort_workspace_size(int T, int top_k, int G);
+
+/*
+ * Dispatch: v = weights[t, j] * x[t] (weights NULL: x[t]) for every pair, in the
+ * row rows[t, j].
+ *   x [T][ld_x >= K]       DG_BF16 or DG_F32, rows 16-byte aligned
+ *   weights [T][top_k]     fp32 or NULL
+ *   rows [T][top_k]        from the sort: each row at most once (not checked;
+ *                          a row outside the layout counts as -1)
+ * Outputs, each optional, at least one; rows that hold no pair are not written,
+ * in y, q and sf:
+ *   y [..][K] bf16
+ *   q [..][K] E4M3, sf     v through the 1x128 quantiser (the _ue8m0 forms: its
+ *                          _ue8m0 form, packed words), in the A operand's layout
+ *                          of the M-grouped GEMMs:
+ *       contiguous: q [M_total][K], sf [K/128][M_total] (packed: [ceil(K/512)])
+ *       masked: q [G][M_cap][K], sf [G][K/128][round_up(M_cap,4)]
+ *   contiguous only, written entirely, zeros on rows that hold no pair:
+ *   qt [M_total][K] E4M3, sft [M_total/128][K] fp32   one scale per column and
+ *       128 rows (power-of-two scales in the _ue8m0 forms): an operand of
+ *       dg_k_grouped_fp8_gemm_tn_contiguous (for the weight gradient); needs src
+ *       (the sort's, of the same rows)
+ * Errors: DG_ERR_NULL; DG_ERR_SHAPE (T < 0; top_k, G, M_cap < 1; M_total < 0 or
+ * % 128; K < 128, K % 128, K > 16384; T * top_k or the rows reaching 2^31);
+ * DG_ERR_ARG (x_type); DG_ERR_ALIGN.
+ */
+int dg_moe_dispatch_quantize_e4m3_contiguous(const void *x, int x_type, int64_t ld_x, const float *weights,
+                                             const int32_t *rows, const int32_t *src,
+                                             uint16_t *y, uint8_t *q, float *sf, uint8_t *qt, float *sft,
+                                             int T, int top_k, int K, int M_total, void *stream);
+int dg_moe_dispatch_quantize_e4m3_contiguous_ue8m0(const void *x, int x_type, int64_t ld_x, const float *weights,
+                                                   const int32_t *rows, const int32_t *src,
+                                                   uint16_t *y, uint8_t *q, float *sf, uint8_t *qt, float *sft,
+                                                   int T, int top_k, int K, int M_total, void *stream);
+int dg_moe_dispatch_quantize_e4m3_contiguous_ue8m0_packed(const void *x, int x_type, int64_t ld_x,
+                                                          const float *weights,
+                                                          const int32_t *rows, const int32_t *src,
+                                                          uint16_t *y, uint8_t *q, uint32_t *sf,
+                                                          uint8_t *qt, float *sft,
+                                                          int T, int top_k, int K, int M_total, void *stream);
+int dg_moe_dispatch_quantize_e4m3_masked(const void *x, int x_type, int64_t ld_x, const float *weights,
+                                         const int32_t *rows, uint16_t *y, uint8_t *q, float *sf,
+                                         int T, int top_k, int K, int G, int M_cap, void *stream);
+int dg_moe_dispatch_quantize_e4m3_masked_ue8m0(const void *x, int x_type, int64_t ld_x, const float *weights,
+                                               const int32_t *rows, uint16_t *y, uint8_t *q, float *sf,
+                                               int T, int top_k, int K, int G, int M_cap, void *stream);
+int dg_moe_dispatch_quantize_e4m3_masked_ue8m0_packed(const void *x, int x_type, int64_t ld_x, const float *weights,
+                                                      const int32_t *rows, uint16_t *y, uint8_t *q, uint32_t *sf,
+                                                      int T, int top_k, int K, int G, int M_cap, void *stream);
+
+/*
+ * Dispatch of codes that are quantised already (a norm's, or another rank's):
+ * codes and scales are copied as they are.
+ *   q_in [T][K] E4M3;  sf_in [K/128][ld_in] fp32, or packed words [ceil(K/512)][ld_in]
+ *   (ld_in >= T, a multiple of 4); q, sf as above, sf in sf_in's format.
+ * Errors as above (K of any multiple of 128).
+ */
+int dg_moe_dispatch_e4m3_contiguous(const uint8_t *q_in, const float *sf_in, int ld_in, const int32_t *rows,
+                                    uint8_t *q, float *sf, int T, int top_k, int K, int M_total, void *stream);
+int dg_moe_dispatch_e4m3_contiguous_ue8m0_packed(const uint8_t *q_in, const uint32_t *sf_in, int ld_in,
+                                                 const int32_t *rows, uint8_t *q, uint32_t *sf,
+                                                 int T, int top_k, int K, int M_total, void *stream);
+int dg_moe_dispatch_e4m3_masked(const uint8_t *q_in, const float *sf_in, int ld_in, const int32_t *rows,
+                                uint8_t *q, float *sf, int T, int top_k, int K, int G, int M_cap, void *stream);
+int dg_moe_dispatch_e4m3_masked_ue8m0_packed(const uint8_t *q_in, const uint32_t *sf_in, int ld_in,
+                                             const int32_t *rows, uint8_t *q, uint32_t *sf,
+                                             int T, int top_k, int K, int G, int M_cap, void *stream);
+
+/*
+ * Combine: the experts' rows back to their tokens,
+ *   out[t] = residual[t] + sum_j weights[t, j] * y[rows[t, j]]
+ * summed in fp32 in the order of the choices and rounded once.
+ *   y [R][K] bf16          the experts' outputs (R = M_total, or G * M_cap)
+ *   weights [T][top_k]     fp32 or NULL (ones: the gradient of dispatch without
+ *                          weights)
+ *   residual, out [T][K]   out_type DG_BF16 or DG_F32; residual NULL = 0, and
+ *                          may be out (in place)
+ * Errors: DG_ERR_NULL; DG_ERR_SHAPE (T, R < 0; top_k < 1; K < 8 or K % 8;
+ * T * top_k reaching 2^31); DG_ERR_ARG (out_type); DG_ERR_ALIGN.
+ */
+int dg_moe_combine(const uint16_t *y, const float *weights, const int32_t *rows, const void *residual,
+                   void *out, int out_type, int T, int top_k, int K, int R, void *stream);
+
+/*
+ * Gradient of combine (contiguous layout):
+ *   dw[t, j] = sum_k dout[t, k] * y[rows[t, j], k]         [T][top_k] fp32, optional
+ *   dy[rows[t, j]] = weights[t, j] * dout[t]               a dispatch of dout: its
+ *                                                          outputs dy, q, sf, qt, sft
+ * dout [T][ld_dout >= K] DG_BF16 or DG_F32; y [M_total][K] bf16 (needed for dw);
+ * the gradient of residual is dout.  Arguments, forms and errors as for
+ * dg_moe_dispatch_quantize_e4m3_contiguous; at least one output.
+ */
+int dg_moe_combine_backward_quantize_e4m3_contiguous(const void *dout, int dout_type, int64_t ld_dout,
+                                                     const uint16_t *y, const float *weights,
+                                                     const int32_t *rows, const int32_t *src,
+                                                     float *dw, uint16_t *dy, uint8_t *q, float *sf,
+                                                     uint8_t *qt, float *sft,
+                                                     int T, int top_k, int K, int M_total, void *stream);
+int dg_moe_combine_backward_quantize_e4m3_contiguous_ue8m0(const void *dout, int dout_type, int64_t ld_dout,
+                                                           const uint16_t *y, const float *weights,
+                                                           const int32_t *rows, const int32_t *src,
+                                                           float *dw, uint16_t *dy, uint8_t *q, float *sf,
+                                                           uint8_t *qt, float *sft,
+                                                           int T, int top_k, int K, int M_total, void *stream);
+int dg_moe_combine_backward_quantize_e4m3_contiguous_ue8m0_packed(const void *dout, int dout_type, int64_t ld_dout,
+                                                                  const uint16_t *y, const float *weights,
+                                                                  const int32_t *rows, const int32_t *src,
+                                                                  float *dw, uint16_t *dy, uint8_t *q, uint32_t *sf,
+                                                                  uint8_t *qt, float *sft,
+                                                                  int T, int top_k, int K, int M_total,
+                                                                  void *stream);
 
 /* Row alignment of expert segments in the contiguous layout (128): the
  * set_/get_mk_alignment_for_contiguous_layout utilities of the "DeepGEMM"

@@ -18,6 +18,17 @@ __all__ = [
     "m_grouped_fp8_gated_gemm_nt_contiguous",
     "m_grouped_fp8_gated_gemm_nt_masked",
     "gated_backward_quantize_e4m3",
+    "layernorm_quantize_e4m3_1x128",
+    "layernorm_backward",
+    "get_moe_rows",
+    "moe_sort_contiguous",
+    "moe_sort_masked",
+    "moe_dispatch_quantize_e4m3_contiguous",
+    "moe_dispatch_quantize_e4m3_masked",
+    "moe_dispatch_e4m3_contiguous",
+    "moe_dispatch_e4m3_masked",
+    "moe_combine",
+    "moe_combine_backward_quantize_e4m3_contiguous",
     "get_mk_alignment_for_contiguous_layout",
     "set_mk_alignment_for_contiguous_layout",
     "get_sf_aligned_size",

@@ -114,6 +114,32 @@ EXPORTS = {
        for name in ("dg_m_grouped_fp8_gated_gemm_nt_masked", "dg_m_grouped_fp8_gated_gemm_nt_masked_ue8m0_packed")},
     **{name: (ct.c_int, [_P, _P, ct.c_int, _P, _P, _P, _P, ct.c_int, _P, _P, _P, _P, ct.c_int, ct.c_int, _P])
        for name in ("dg_gated_backward_quantize_e4m3", "dg_gated_backward_quantize_e4m3_ue8m0")},
+    **{name: (ct.c_int, [_P, ct.c_int, ct.c_int64, _P, ct.c_int, _P, _P, ct.c_int, ct.c_float, _P, _P, _P, _P, ct.c_int,
+                         ct.c_int, ct.c_int, _P])
+       for name in ("dg_layernorm_quantize_e4m3_1x128", "dg_layernorm_quantize_e4m3_1x128_ue8m0",
+                    "dg_layernorm_quantize_e4m3_1x128_ue8m0_packed")},
+    "dg_layernorm_backward": (ct.c_int, [_P, ct.c_int, _P, ct.c_int, _P, ct.c_int, ct.c_float, _P, _P, _P, _P, ct.c_int,
+                                         ct.c_int, _P, ct.c_size_t, _P]),
+    "dg_get_layernorm_backward_workspace_size": (ct.c_int64, [ct.c_int, ct.c_int]),
+    "dg_moe_sort_contiguous": (ct.c_int, [_P, ct.c_int, ct.c_int, ct.c_int, _P, _P, _P, _P, _P, ct.c_int, _P, ct.c_size_t,
+                                          _P]),
+    "dg_moe_sort_masked": (ct.c_int, [_P, ct.c_int, ct.c_int, ct.c_int, _P, _P, _P, ct.c_int, _P, ct.c_size_t, _P]),
+    "dg_get_moe_rows": (ct.c_int64, [ct.c_int, ct.c_int, ct.c_int]),
+    "dg_get_moe_sort_workspace_size": (ct.c_int64, [ct.c_int, ct.c_int, ct.c_int]),
+    **{"dg_moe_dispatch_quantize_e4m3_contiguous" + s: (ct.c_int, [_P, ct.c_int, ct.c_int64, _P, _P, _P, _P, _P, _P, _P, _P,
+                                                                   ct.c_int, ct.c_int, ct.c_int, ct.c_int, _P])
+       for s in ("", "_ue8m0", "_ue8m0_packed")},
+    **{"dg_moe_dispatch_quantize_e4m3_masked" + s: (ct.c_int, [_P, ct.c_int, ct.c_int64, _P, _P, _P, _P, _P, ct.c_int,
+                                                               ct.c_int, ct.c_int, ct.c_int, ct.c_int, _P])
+       for s in ("", "_ue8m0", "_ue8m0_packed")},
+    **{"dg_moe_dispatch_e4m3_contiguous" + s: (ct.c_int, [_P, _P, ct.c_int, _P, _P, _P, ct.c_int, ct.c_int, ct.c_int,
+                                                          ct.c_int, _P]) for s in ("", "_ue8m0_packed")},
+    **{"dg_moe_dispatch_e4m3_masked" + s: (ct.c_int, [_P, _P, ct.c_int, _P, _P, _P, ct.c_int, ct.c_int, ct.c_int, ct.c_int,
+                                                      ct.c_int, _P]) for s in ("", "_ue8m0_packed")},
+    "dg_moe_combine": (ct.c_int, [_P, _P, _P, _P, _P, ct.c_int, ct.c_int, ct.c_int, ct.c_int, ct.c_int, _P]),
+    **{"dg_moe_combine_backward_quantize_e4m3_contiguous" + s: (
+        ct.c_int, [_P, ct.c_int, ct.c_int64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ct.c_int, ct.c_int, ct.c_int, ct.c_int,
+                   _P]) for s in ("", "_ue8m0", "_ue8m0_packed")},
     "dg_set_mk_alignment_for_contiguous_layout": (ct.c_int, [ct.c_int]),
     "dg_get_sf_aligned_size": (ct.c_int, [ct.c_int]),
     "dg_set_num_cus": (ct.c_int, [ct.c_int]),
@@ -766,6 +792,311 @@ def gated_backward_quantize_e4m3(gu, dh, act="silu", m_indices=None, dgu=None, q
     _call("dg_gated_backward_quantize_e4m3" + ("_ue8m0" if ue8m0 else ""), p[0], p[1], _act_of(act), p[2], p[3], p[4],
           p[5], ld, p[6], p[7], p[8], p[9], rows, I, _raw_stream(index))
     return dgu, q, sf, qt, sft, ht, sfht
+
+
+_LN_NAMES = ("residual", "weight", "bias", "residual_out", "y", "q", "sf")
+
+
+def layernorm_quantize_e4m3_1x128(x, weight=None, bias=None, eps=1e-5, residual=None, residual_out=None, y=None, q=None,
+                                  sf=None, ld_sf=None, scales="fp32"):
+    """h = x + residual, layer norm of h times weight plus bias, 1x128 E4M3 quantisation, in one pass
+    (dg_layernorm_quantize_e4m3_1x128[_ue8m0[_packed]]).
+
+    Arguments and results as for rmsnorm_quantize_e4m3_1x128; weight and bias [K] of one type (bf16 or fp32), each
+    optional; K a multiple of 128, with q=False of 8."""
+    suffix = _SUFFIX.get(scales)
+    if suffix is None:
+        raise ValueError(f"scales {scales!r}, expected one of {tuple(_SUFFIX)}")
+    if x.dim() != 2:
+        raise ValueError("x: must have two dimensions, [rows, K]")
+    shape = x.shape
+    rows, K = shape
+    pitch, column = x.stride()
+    if column != 1 and K > 1:
+        raise ValueError("x: columns must be dense")
+    index = _device(x, "x")
+    res_type = 0
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+    else:
+        res_type = _type_of(residual, "residual")
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+    w_type = 0
+    if weight is not None:
+        w_type = _type_of(weight, "weight")
+    elif bias is not None:
+        w_type = _type_of(bias, "bias")
+    if y is True:
+        y = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+    packed = scales == "ue8m0_packed"
+    ld, sf_shape = 0, ()
+    if q is False:
+        q = sf = None
+    else:
+        ld = (sf.shape[-1] if sf is not None else (rows + 3) // 4 * 4) if ld_sf is None else int(ld_sf)
+        sf_shape = (_sf_rows(packed, K // 128), ld)
+        if q is None:
+            q = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        if sf is None:
+            sf = torch.zeros(sf_shape, dtype=torch.int32 if packed else torch.float32, device=x.device)
+    res_bits, w_bits = _F32 if res_type else _BF16, _F32 if w_type else _BF16
+    p = _pointers(index, _LN_NAMES, residual, res_bits, shape, weight, w_bits, (K,), bias, w_bits, (K,), residual_out,
+                  res_bits, shape, y, _BF16, shape, q, _E4M3, shape, sf, _I32 if packed else _F32, sf_shape)
+    _call("dg_layernorm_quantize_e4m3_1x128" + suffix, x.data_ptr(), _type_of(x, "x"), pitch if rows > 1 else K, p[0],
+          res_type, p[1], p[2], w_type, eps, p[3], p[4], p[5], p[6], ld, rows, K, _raw_stream(index))
+    return q, sf, residual_out, y
+
+
+def get_layernorm_backward_workspace_size(rows: int, K: int) -> int:
+    """Bytes of scratch layernorm_backward needs on the current device (of any content)."""
+    v = lib().dg_get_layernorm_backward_workspace_size(int(rows), int(K))
+    if v < 0:
+        raise DGError(int(v), "dg_get_layernorm_backward_workspace_size")
+    return int(v)
+
+
+_LN_BWD_NAMES = ("dy", "h", "weight", "dres", "dx", "dw", "db")
+
+
+def layernorm_backward(dy, h, weight=None, eps=1e-5, dres=None, dx=None, dw=None, db=None, workspace="auto"):
+    """Gradient of the layer norm (dg_layernorm_backward): dy[rows, K] bf16 or fp32, h[rows, K] the norm's input as stored
+    (bf16 or fp32), weight[K] or None (ones), dres[rows, K] of h's type the gradient arriving at h itself (or None);
+    returns (dx of h's type, dw[K], db[K] fp32), each a tensor to fill or a new one; dw=False and db=False leave them
+    out.  dx may be dres or h.  workspace: a uint8 device tensor of get_layernorm_backward_workspace_size bytes, or
+    "auto"."""
+    shape = h.shape
+    if len(shape) != 2:
+        raise ValueError(f"h: shape {tuple(shape)}, expected [rows, K]")
+    rows, K = shape
+    if isinstance(workspace, str) and workspace != "auto":
+        raise ValueError(f"workspace {workspace!r}")
+    index = _device(h, "h")
+    h_type = _type_of(h, "h")
+    dw = _out(True if dw is None else dw, (K,), torch.float32, h.device)
+    db = _out(True if db is None else db, (K,), torch.float32, h.device)
+    if isinstance(workspace, str):
+        n = get_layernorm_backward_workspace_size(rows, K) if dw is not None or db is not None else 0
+        workspace = torch.empty(n, dtype=torch.uint8, device=h.device) if n else None
+    if dx is None:
+        dx = torch.empty_like(h)
+    bits = _F32 if h_type else _BF16
+    p = _pointers(index, _LN_BWD_NAMES, dy, _REAL, shape, h, bits, shape, weight, _REAL, (K,), dres, bits, shape,
+                  dx, bits, shape, dw, _F32, (K,), db, _F32, (K,))
+    _call("dg_layernorm_backward", p[0], _type_of(dy, "dy"), p[1], h_type, p[2],
+          0 if weight is None else _type_of(weight, "weight"), eps, p[3], p[4], p[5], p[6], rows, K,
+          *_workspace(workspace, index), _raw_stream(index))
+    return dx, dw, db
+
+
+# ---------------------------------------------------------------- tokens to the experts' rows and back
+
+def get_moe_rows(T: int, top_k: int, G: int) -> int:
+    """Rows of the contiguous layout that hold T * top_k pairs however they fall on G experts (dg_get_moe_rows)."""
+    v = lib().dg_get_moe_rows(int(T), int(top_k), int(G))
+    if v < 0:
+        raise DGError(int(v), "dg_get_moe_rows")
+    return int(v)
+
+
+def get_moe_sort_workspace_size(T: int, top_k: int, G: int) -> int:
+    """Bytes of scratch (of any content) that the sort of T * top_k pairs uses (0: none)."""
+    v = lib().dg_get_moe_sort_workspace_size(int(T), int(top_k), int(G))
+    if v < 0:
+        raise DGError(int(v), "dg_get_moe_sort_workspace_size")
+    return int(v)
+
+
+def _sort_workspace(workspace, T, top_k, G, device):
+    if not isinstance(workspace, str):
+        return workspace
+    if workspace != "auto":
+        raise ValueError(f"workspace {workspace!r}")
+    # up to 2^15 pairs are sorted without one: no call to ask
+    n = get_moe_sort_workspace_size(T, top_k, G) if T * top_k > 32768 else 0
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def moe_sort_contiguous(ids, G, M_total=None, rows=None, src=None, m_indices=None, counts=None, ks=None, workspace="auto"):
+    """A row of the contiguous layout for every (token, choice) pair (dg_moe_sort_contiguous): ids[T, top_k] int32, an id
+    outside [0, G) has no row.  M_total: rows of the layout, get_moe_rows(T, top_k, G) when None.  Outputs, each an int32
+    tensor to fill; rows[T, top_k] and m_indices[M_total] are new ones when None, src[M_total] (the pair of each row),
+    counts[G] and ks[G] (padded sizes) when True.  Returns (rows, src, m_indices, counts, ks), None where not asked
+    for."""
+    if ids.dim() != 2:
+        raise ValueError("ids[T, top_k]")
+    T, top_k = ids.shape
+    index = _device(ids, "ids")
+    if M_total is None:
+        M_total = get_moe_rows(T, top_k, G)
+    i32, dev = torch.int32, ids.device
+    if rows is None or m_indices is None or src is True or counts is True or ks is True:
+        rows = _out(True if rows is None else rows, (T, top_k), i32, dev)
+        m_indices = _out(True if m_indices is None else m_indices, (M_total,), i32, dev)
+        src, counts, ks = _out(src, (M_total,), i32, dev), _out(counts, (G,), i32, dev), _out(ks, (G,), i32, dev)
+    workspace = _sort_workspace(workspace, T, top_k, G, dev)
+    p = _pointers(index, ("ids", "rows", "src", "m_indices", "counts", "ks"), ids, _I32, (T, top_k), rows, _I32, (T, top_k),
+                  src, _I32, (M_total,), m_indices, _I32, (M_total,), counts, _I32, (G,), ks, _I32, (G,))
+    _call("dg_moe_sort_contiguous", p[0], T, top_k, G, p[1], p[2], p[3], p[4], p[5], M_total, *_workspace(workspace, index),
+          _raw_stream(index))
+    return rows, src, m_indices, counts, ks
+
+
+def moe_sort_masked(ids, G, M_cap, rows=None, src=None, masked_m=None, workspace="auto"):
+    """A row of the masked layout, expert * M_cap + position, for every (token, choice) pair (dg_moe_sort_masked); pairs
+    past M_cap have none (-1).  rows[T, top_k] and masked_m[G] are new int32 tensors when None, src[G, M_cap] when True.
+    Returns (rows, src, masked_m)."""
+    if ids.dim() != 2:
+        raise ValueError("ids[T, top_k]")
+    T, top_k = ids.shape
+    index = _device(ids, "ids")
+    i32, dev = torch.int32, ids.device
+    if rows is None or masked_m is None or src is True:
+        rows = _out(True if rows is None else rows, (T, top_k), i32, dev)
+        masked_m = _out(True if masked_m is None else masked_m, (G,), i32, dev)
+        src = _out(src, (G, M_cap), i32, dev)
+    workspace = _sort_workspace(workspace, T, top_k, G, dev)
+    p = _pointers(index, ("ids", "rows", "src", "masked_m"), ids, _I32, (T, top_k), rows, _I32, (T, top_k),
+                  src, _I32, (G, M_cap), masked_m, _I32, (G,))
+    _call("dg_moe_sort_masked", p[0], T, top_k, G, p[1], p[2], p[3], M_cap, *_workspace(workspace, index),
+          _raw_stream(index))
+    return rows, src, masked_m
+
+
+_DISPATCH_NAMES = ("rows", "src", "weights", "y", "q", "sf", "qt", "sft", "ye", "dw")
+
+
+def _dispatch(name, x, rows, lead, per, src, weights, y, q, sf, qt, sft, scales, ye=None, dw=None):
+    """What the quantising dispatches and combine's gradient share: lead = leading dimensions of the experts' rows, per =
+    rows of a group.  Returns (the C call's arguments, the outputs)."""
+    suffix = _SUFFIX.get(scales)
+    if suffix is None:
+        raise ValueError(f"scales {scales!r}, expected one of {tuple(_SUFFIX)}")
+    if x.dim() != 2 or rows.dim() != 2:
+        raise ValueError(f"{name}[T, K], rows[T, top_k]")
+    T, K = x.shape
+    pitch, column = x.stride()
+    if column != 1 and K > 1:
+        raise ValueError(f"{name}: columns must be dense")
+    index = _device(x, name)
+    packed = scales == "ue8m0_packed"
+    f32, dev = torch.float32, x.device
+    pairs = rows.shape
+    ld = (per + 3) // 4 * 4
+    shape, shape_sf = (*lead, per, K), (*lead, _sf_rows(packed, K // 128), ld)
+    if q is None and y is None and qt is None and dw is None:
+        q = True
+    if q is True or y is True or qt is True or dw is True:
+        y, q = _out(y, shape, torch.bfloat16, dev, True), _out(q, shape, torch.uint8, dev, True)
+        qt, dw = _out(qt, shape, torch.uint8, dev), _out(dw, pairs, f32, dev)
+    if q is None or q is False:
+        q = sf = None
+    elif sf is None or sf is True:
+        sf = torch.zeros(shape_sf, dtype=torch.int32 if packed else f32, device=dev)
+    if qt is None or qt is False:
+        qt = sft = None
+    elif sft is None or sft is True:
+        sft = torch.empty((per // 128, K), dtype=f32, device=dev)
+    p = _pointers(index, _DISPATCH_NAMES, rows, _I32, (T, rows.shape[1]), src, _I32, (per,), weights, _F32, pairs,
+                  y, _BF16, shape, q, _E4M3, shape, sf, _I32 if packed else _F32, shape_sf, qt, _E4M3, shape,
+                  sft, _F32, (per // 128, K), ye, _BF16, shape, dw, _F32, pairs)
+    return p, (x.data_ptr(), _type_of(x, name), pitch if T > 1 else K), (T, pairs[1], K), suffix, (q, sf, qt, sft, y, dw), index
+
+
+def moe_dispatch_quantize_e4m3_contiguous(x, rows, M_total, src=None, weights=None, y=None, q=None, sf=None, qt=None,
+                                          sft=None, scales="fp32"):
+    """Tokens to their experts' rows of the contiguous layout, quantised (dg_moe_dispatch_quantize_e4m3_contiguous[_ue8m0
+    [_packed]]): x[T, K] bf16 or fp32 (rows may be strided), rows[T, top_k] int32 from moe_sort_contiguous,
+    weights[T, top_k] fp32 or None: row rows[t, j] holds weights[t, j] * x[t].  Outputs, each a tensor to fill or True for
+    a new one: q[M_total, K] E4M3 (the default) with sf[K/128, M_total] (scales "ue8m0_packed": int32
+    [ceil(K/512), M_total]), y[M_total, K] bf16, and qt[M_total, K] with sft[M_total/128, K], one scale per column and 128
+    rows (needs src[M_total] from the sort).  Rows that hold no pair are zeros in qt; in the others they keep what the
+    buffers held (new ones: zeros).  Returns (q, sf, qt, sft, y), None where not asked for."""
+    p, lead, sizes, suffix, out, index = _dispatch("x", x, rows, (), M_total, src, weights, y, q, sf, qt, sft, scales)
+    _call("dg_moe_dispatch_quantize_e4m3_contiguous" + suffix, *lead, p[2], p[0], p[1], p[3], p[4], p[5], p[6], p[7], *sizes,
+          M_total, _raw_stream(index))
+    return out[:5]
+
+
+def moe_dispatch_quantize_e4m3_masked(x, rows, G, M_cap, weights=None, y=None, q=None, sf=None, scales="fp32"):
+    """The same in the masked layout (rows from moe_sort_masked): q[G, M_cap, K] with sf[G, K/128, round_up(M_cap, 4)]
+    (packed: [G, ceil(K/512), ..]), y[G, M_cap, K].  Returns (q, sf, y)."""
+    p, lead, sizes, suffix, out, index = _dispatch("x", x, rows, (G,), M_cap, None, weights, y, q, sf, None, None, scales)
+    _call("dg_moe_dispatch_quantize_e4m3_masked" + suffix, *lead, p[2], p[0], p[3], p[4], p[5], *sizes, G, M_cap,
+          _raw_stream(index))
+    return out[0], out[1], out[4]
+
+
+def _dispatch_codes(q_in, sf_in, rows, lead, per, q, sf):
+    if q_in.dim() != 2 or rows.dim() != 2 or sf_in.dim() != 2:
+        raise ValueError("q_in[T, K], sf_in[K/128, ld], rows[T, top_k]")
+    T, K = q_in.shape
+    index = _device(q_in, "q_in")
+    packed = sf_in.dtype is torch.int32
+    n, bits, ld = _sf_rows(packed, K // 128), _I32 if packed else _F32, (per + 3) // 4 * 4
+    if q is None:
+        q = torch.zeros((*lead, per, K), dtype=torch.uint8, device=q_in.device)
+    if sf is None:
+        sf = torch.zeros((*lead, n, ld), dtype=sf_in.dtype, device=q_in.device)
+    p = _pointers(index, ("q_in", "sf_in", "rows", "q", "sf"), q_in, _E4M3, (T, K), sf_in, bits, (n, sf_in.shape[1]),
+                  rows, _I32, (T, rows.shape[1]), q, _E4M3, (*lead, per, K), sf, bits, (*lead, n, ld))
+    return (p[0], p[1], sf_in.shape[1], p[2], p[3], p[4], T, rows.shape[1], K), q, sf, "_ue8m0_packed" if packed else "", index
+
+
+def moe_dispatch_e4m3_contiguous(q_in, sf_in, rows, M_total, q=None, sf=None):
+    """Codes that are quantised already, to their experts' rows (dg_moe_dispatch_e4m3_contiguous[_ue8m0_packed]):
+    q_in[T, K] E4M3, sf_in[K/128, ld] fp32 or [ceil(K/512), ld] int32 (packed), as a norm or a quantiser writes them;
+    q[M_total, K], sf[.., M_total] in sf_in's format.  Returns (q, sf)."""
+    args, q, sf, suffix, index = _dispatch_codes(q_in, sf_in, rows, (), M_total, q, sf)
+    _call("dg_moe_dispatch_e4m3_contiguous" + suffix, *args, M_total, _raw_stream(index))
+    return q, sf
+
+
+def moe_dispatch_e4m3_masked(q_in, sf_in, rows, G, M_cap, q=None, sf=None):
+    """The same in the masked layout: q[G, M_cap, K], sf[G, .., round_up(M_cap, 4)].  Returns (q, sf)."""
+    args, q, sf, suffix, index = _dispatch_codes(q_in, sf_in, rows, (G,), M_cap, q, sf)
+    _call("dg_moe_dispatch_e4m3_masked" + suffix, *args, G, M_cap, _raw_stream(index))
+    return q, sf
+
+
+def moe_combine(y, rows, weights=None, residual=None, out=None):
+    """The experts' rows back to their tokens (dg_moe_combine): out[t] = residual[t] + sum_j weights[t, j] * y[rows[t, j]].
+    y[.., K] bf16 (any leading dimensions, R rows in all), rows[T, top_k] int32, weights[T, top_k] fp32 or None (ones),
+    residual[T, K] bf16 or fp32 or None; out[T, K] of the residual's type (a new one when None: bf16 without residual),
+    may be the residual.  Returns out."""
+    if rows.dim() != 2 or y.dim() < 2:
+        raise ValueError("y[.., K], rows[T, top_k]")
+    pairs = rows.shape
+    T, K = pairs[0], y.shape[-1]
+    index = _device(y, "y")
+    if out is None:
+        out = torch.empty((T, K), dtype=torch.bfloat16 if residual is None else residual.dtype, device=y.device)
+    out_type = _type_of(out, "out")
+    bits = _F32 if out_type else _BF16
+    p = _pointers(index, ("y", "weights", "rows", "residual", "out"), y, _BF16, y.shape, weights, _F32, pairs, rows, _I32,
+                  pairs, residual, bits, (T, K), out, bits, (T, K))
+    _call("dg_moe_combine", p[0], p[1], p[2], p[3], p[4], out_type, T, pairs[1], K, y.numel() // K if K else 0,
+          _raw_stream(index))
+    return out
+
+
+def moe_combine_backward_quantize_e4m3_contiguous(dout, y, rows, weights=None, src=None, dw=None, dy=None, q=None, sf=None,
+                                                  qt=None, sft=None, scales="fp32"):
+    """Gradient of moe_combine in the contiguous layout (dg_moe_combine_backward_quantize_e4m3_contiguous[_ue8m0[_packed]]):
+    dout[T, K] bf16 or fp32 (rows may be strided), y[M_total, K] bf16 the experts' rows.  dw[T, top_k] fp32, the weights'
+    gradient, and the rows' gradient weights[t, j] * dout[t] as a dispatch: dy bf16, q with sf, qt with sft (needs src).
+    Each a tensor to fill or True for a new one.  Returns (dw, dy, q, sf, qt, sft), None where not asked for."""
+    if y.dim() != 2:
+        raise ValueError("y[M_total, K]")
+    M_total = y.shape[0]
+    if dw is False:
+        dw = None
+    p, lead, sizes, suffix, out, index = _dispatch("dout", dout, rows, (), M_total, src, weights, dy, q, sf, qt, sft, scales,
+                                                   ye=y, dw=dw)
+    _call("dg_moe_combine_backward_quantize_e4m3_contiguous" + suffix, *lead, p[8], p[2], p[0], p[1], p[9], p[3], p[4], p[5],
+          p[6], p[7], *sizes, M_total, _raw_stream(index))
+    return out[5], out[4], out[0], out[1], out[2], out[3]
 
 
 def get_mk_alignment_for_contiguous_layout() -> int:

@@ -1,5 +1,6 @@
 // dg_layer.h -- host-side declarations of the feed-forward layer's kernels:
-// the RMS norm, the gated GEMM and their gradients.
+// the norms, the gated GEMM, the tokens' way to the experts' rows and back, and
+// their gradients.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -49,6 +50,89 @@ struct RmsNormBwdProblem {
 };
 size_t rmsnorm_bwd_workspace(int rows, int K, int num_cus);
 hipError_t launch_rmsnorm_bwd(const RmsNormBwdProblem &p, int num_cus, hipStream_t stream);
+
+struct LayerNormProblem {
+    const void *x, *residual, *weight, *bias;
+    void *residual_out;
+    uint16_t *y;
+    uint8_t *q;
+    void *sf;
+    int64_t ld_x;
+    int rows, K, ld_sf;
+    float eps;
+    int x_type, res_type, w_type, format;
+};
+// Needs rows >= 1, K a multiple of 8 (with q: of 128) up to kNormMaxK.
+hipError_t launch_layernorm_quant(const LayerNormProblem &p, hipStream_t stream);
+
+struct LayerNormBwdProblem {
+    const void *dy, *h, *weight, *dres;
+    void *dx;
+    float *dw, *db;
+    void *ws;
+    int rows, K;
+    float eps;
+    int h_type, dy_type, w_type;
+};
+size_t layernorm_bwd_workspace(int rows, int K, int num_cus);
+hipError_t launch_layernorm_bwd(const LayerNormBwdProblem &p, int num_cus, hipStream_t stream);
+
+// Rows of the n pairs ids[0 .. n) sorted by expert: R rows in segments of whole
+// 128-row blocks (cap = 0) or of cap rows.  counts: pairs that have a row,
+// ks: padded sizes.
+constexpr int kMoeMaxExperts = 1024;
+struct MoeSortProblem {
+    const int32_t *ids;
+    int32_t *rows, *src, *expert, *counts, *ks;
+    void *ws;
+    size_t ws_bytes;
+    int n, G, cap, R;
+};
+// Needs 1 <= G <= kMoeMaxExperts, n + 128 G and R below 2^31.
+size_t moe_sort_workspace(int64_t n, int G);
+hipError_t launch_moe_sort(const MoeSortProblem &p, hipStream_t stream);
+
+// Tokens to the experts' rows; with ye and dw also dw[t, j] = x[t] . ye[rows[t, j]].
+// Groups of cap rows (contiguous: R), sf_group scale words each.
+struct MoeDispatchProblem {
+    const void *x;
+    const float *weights;
+    const int32_t *rows, *src;
+    const uint16_t *ye;
+    float *dw;
+    uint16_t *y;
+    uint8_t *q;
+    void *sf;
+    uint8_t *qt;
+    float *sft;
+    int64_t ld_x, sf_group;
+    int T, top_k, K, R, cap, ld_sf, x_type, format;
+};
+// Needs K a multiple of 128 up to kNormMaxK; with qt one group, R a multiple of 128.
+hipError_t launch_moe_dispatch(const MoeDispatchProblem &p, hipStream_t stream);
+
+struct MoeCopyProblem {
+    const uint8_t *x;
+    const uint32_t *sf_in;
+    const int32_t *rows;
+    uint8_t *q;
+    uint32_t *sf;
+    int64_t sf_group;
+    int T, top_k, K, R, cap, ld_in, ld_sf, words;
+};
+// Needs T >= 1, K a multiple of 128.
+hipError_t launch_moe_dispatch_codes(const MoeCopyProblem &p, hipStream_t stream);
+
+struct MoeCombineProblem {
+    const uint16_t *y;
+    const float *weights;
+    const int32_t *rows;
+    const void *residual;
+    void *out;
+    int T, top_k, K, R, out_type;
+};
+// Needs T >= 1, K a multiple of 8.
+hipError_t launch_moe_combine(const MoeCombineProblem &p, hipStream_t stream);
 
 // Gated GEMM: h = act(A Wg^T) * (A Wu^T).  Per group, A has `rows_a` rows
 // (dense: M, contiguous: M_total, masked: M_cap); `idx` is m_indices

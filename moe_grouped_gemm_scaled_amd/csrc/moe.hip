@@ -1,0 +1,648 @@
+// moe.hip -- tokens to the experts' rows and back, for gfx950.
+//
+// With T tokens, top_k choices each and G experts, a pair p = t * top_k + j is
+// a token's j-th choice.  The sort gives every pair a row of the experts'
+// layout (contiguous: segments of whole 128-row blocks, masked: M_cap rows per
+// expert), in pair order within an expert:
+//     rows[p] = start[e] + |{p' < p : ids[p'] = ids[p] = e}|
+// dispatch:  row rows[t, j] of q, sf = quantise(w[t, j] * x[t])
+// combine:   out[t] = residual[t] + sum_j w[t, j] * y[rows[t, j]]
+// gradient of combine:  dw[t, j] = dout[t] . y[rows[t, j]],
+//                       dy[rows[t, j]] = w[t, j] * dout[t]  (a dispatch)
+// (and combine without weights is the gradient of dispatch).
+//
+// Everything but the sort is HBM-bound.
+#include "dg_codes8.h"
+
+namespace dg {
+
+// ---------------------------------------------------------------- sort
+
+struct SortArgs {
+    const int32_t *ids;
+    int32_t *rows, *src, *expert, *counts, *ks;
+    int32_t *hist;       // per workgroup and expert, from the counting kernel; NULL: counted here
+    int n, G, cap, R, chunk;
+};
+
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+
+// Counts of every chunk's ids, for sorts of so many pairs that each workgroup
+// counting all of them would take longer than a second launch.
+__global__ void __launch_bounds__(kSortThreads) moe_count_kernel(SortArgs p) {
+    extern __shared__ int32_t bins[];
+    for (int e = threadIdx.x; e < p.G; e += kSortThreads) bins[e] = 0;
+    __syncthreads();
+    const int lo = blockIdx.x * p.chunk, hi = (int)min((int64_t)lo + p.chunk, (int64_t)p.n);
+    for (int i = lo + threadIdx.x; i < hi; i += kSortThreads) {
+        const int e = p.ids[i];
+        if ((unsigned)e < (unsigned)p.G) atomicAdd(&bins[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.G; e += kSortThreads) p.hist[(int64_t)blockIdx.x * p.G + e] = bins[e];
+}
+
+// Lanes of the wave that hold the same key (below 2^bits) as this one.
+__device__ __forceinline__ uint64_t same_key(int key, int bits) {
+    uint64_t m = ~0ull;
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (key >> b) & 1;
+        const uint64_t v = __ballot(one);
+        m &= one ? v : ~v;
+    }
+    return m;
+}
+
+// A stable counting sort: workgroup b ranks the pairs of its chunk.  It needs
+// the counts of the pairs before the chunk (ranks) and of all pairs (starts);
+// within the chunk, wave w ranks a run of consecutive pairs, 64 at a time, from
+// ballots over the bits of their keys, and the waves' counts are added up in
+// order.  No result depends on the order in which anything runs: LDS atomics
+// only count.
+//
+// LDS: before[G], total[G], start[G] (32 bits) and the waves' counts [16][G]
+// (16 bits: a chunk is at most 2^15 pairs).
+__global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(SortArgs p) {
+    extern __shared__ int32_t lds[];
+    const int G = p.G, t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    int32_t *before = lds, *total = lds + G, *start = lds + 2 * G;
+    uint16_t *hist = reinterpret_cast<uint16_t *>(lds + 3 * G);
+    __shared__ int32_t scan[kSortWaves];
+    for (int e = t; e < 3 * G; e += kSortThreads) lds[e] = 0;
+    for (int e = t; e < kSortWaves * G; e += kSortThreads) hist[e] = 0;
+    __syncthreads();
+    const int lo = blockIdx.x * p.chunk, hi = (int)min((int64_t)lo + p.chunk, (int64_t)p.n);
+    // ---- counts of the pairs before the chunk, and of those behind it
+    if (p.hist) {
+        const int n = (int)gridDim.x;
+        for (int i = t; i < n * G; i += kSortThreads) {
+            const int b = i / G, e = i - b * G, c = p.hist[i];
+            if (c) atomicAdd(b < (int)blockIdx.x ? &before[e] : &total[e], b == (int)blockIdx.x ? 0 : c);
+        }
+    } else {
+        auto count = [&](int from, int to, int32_t *bins) __attribute__((always_inline)) {
+#pragma unroll 4
+            for (int i = from + t; i < to; i += kSortThreads) {
+                const int e = p.ids[i];
+                if ((unsigned)e < (unsigned)G) atomicAdd(&bins[e], 1);
+            }
+        };
+        count(0, lo, before);
+        count(hi, p.n, total);
+    }
+    // ---- ranks within the wave's run
+    constexpr int kMostRounds = 8;                     // chunk <= 8192
+    const int rounds = p.chunk / kSortThreads;
+    const int bits = 32 - __clz(G);                    // keys 0 .. G, G: no expert
+    uint16_t *mine = hist + wave * G;
+    int key[kMostRounds], rank[kMostRounds];
+    static_for<kMostRounds>([&](auto rc) __attribute__((always_inline)) {
+        constexpr int r = decltype(rc)::value;
+        if (r < rounds) {                              // uniform
+            const int i = lo + (wave * rounds + r) * 64 + lane;
+            const int e = i < hi ? p.ids[i] : -1;
+            key[r] = (unsigned)e < (unsigned)G ? e : G;
+            const uint64_t m = same_key(key[r], bits);
+            const int below = __popcll(m & ((1ull << lane) - 1));
+            rank[r] = 0;
+            if (key[r] < G) {
+                // one wave's LDS accesses stay in order: all lanes read, then the first writes
+                const int had = *reinterpret_cast<volatile uint16_t *>(&mine[key[r]]);
+                __builtin_amdgcn_wave_barrier();
+                rank[r] = had + below;
+                if (below == 0) *reinterpret_cast<volatile uint16_t *>(&mine[key[r]]) = (uint16_t)(had + __popcll(m));
+            }
+        }
+    });
+    __syncthreads();
+    // ---- the waves' counts become offsets; totals and padded sizes
+    int32_t sum = 0;
+    if (t < G) {
+        int run = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int c = hist[w * G + t];
+            hist[w * G + t] = (uint16_t)run;
+            run += c;
+        }
+        total[t] += before[t] + run;
+        sum = p.cap ? 0 : (total[t] + 127) & ~127;
+    }
+    // ---- starts: an exclusive scan of the padded sizes (G <= 1024 threads)
+    if (p.cap) {
+        if (t < G) start[t] = t * p.cap;
+    } else {
+        int inc = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(inc, d);
+            if (lane >= d) inc += v;
+        }
+        if (lane == 63) scan[wave] = inc;
+        __syncthreads();
+        int base = 0;
+        for (int w = 0; w < wave; ++w) base += scan[w];
+        if (t < G) start[t] = base + inc - sum;
+    }
+    __syncthreads();
+    auto room = [&](int e) __attribute__((always_inline)) { return p.cap ? p.cap : max(p.R - start[e], 0); };
+    if (blockIdx.x == 0 && t < G) {
+        if (p.counts) p.counts[t] = min(total[t], room(t));
+        if (p.ks) p.ks[t] = min((total[t] + 127) & ~127, room(t));
+    }
+    static_for<kMostRounds>([&](auto rc) __attribute__((always_inline)) {
+        constexpr int r = decltype(rc)::value;
+        if (r < rounds) {
+            const int i = lo + (wave * rounds + r) * 64 + lane;
+            if (i < hi) {
+                const int e = key[r];
+                int row = -1;
+                if (e < G) {
+                    const int at = before[e] + hist[wave * G + e] + rank[r];
+                    if (at < room(e)) row = start[e] + at;
+                }
+                p.rows[i] = row;
+                if (p.src && row >= 0) p.src[row] = i;
+            }
+        }
+    });
+    // ---- this workgroup's share of the rows: the expert of each, and -1 where there is none
+    if (!p.src && !p.expert) return;
+    const int r_lo = (int)((int64_t)p.R * blockIdx.x / gridDim.x), r_hi = (int)((int64_t)p.R * (blockIdx.x + 1) / gridDim.x);
+    for (int r = r_lo + t; r < r_hi; r += kSortThreads) {
+        int a = 0;                                     // the last expert that starts at or before r
+        if (p.cap) {
+            a = r / p.cap;
+        } else {
+            int b = G;
+            while (b - a > 1) {
+                const int m = (a + b) >> 1;
+                if (start[m] <= r) a = m;
+                else b = m;
+            }
+        }
+        const bool held = r - start[a] < total[a];
+        if (p.expert) p.expert[r] = held ? a : -1;
+        if (p.src && !held) p.src[r] = -1;
+    }
+}
+
+// Pairs per workgroup: 1024, more only where that would be more than 64
+// workgroups.
+static int sort_chunk(int64_t n) {
+    int chunk = kSortThreads;
+    while (chunk < 8 * kSortThreads && n > (int64_t)64 * chunk) chunk *= 2;
+    return chunk;
+}
+
+constexpr int64_t kSortOneLaunch = 32768;
+
+size_t moe_sort_workspace(int64_t n, int G) {
+    if (n <= kSortOneLaunch) return 0;
+    const int64_t groups = (n + sort_chunk(n) - 1) / sort_chunk(n);
+    return (size_t)groups * G * sizeof(int32_t);
+}
+
+hipError_t launch_moe_sort(const MoeSortProblem &p, hipStream_t stream) {
+    const int chunk = sort_chunk(p.n);
+    int64_t groups = ((int64_t)p.n + chunk - 1) / chunk;
+    if (groups < 1) groups = 1;                        // no pairs: the rows are filled all the same
+    if (!grid_fits(groups, kSortThreads)) return hipErrorInvalidValue;
+    const size_t need = moe_sort_workspace(p.n, p.G);
+    SortArgs a{p.ids, p.rows, p.src, p.expert, p.counts, p.ks, nullptr, p.n, p.G, p.cap, p.R, chunk};
+    if (need && p.ws && p.ws_bytes >= need) {
+        a.hist = static_cast<int32_t *>(p.ws);
+        hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)groups), dim3(kSortThreads), p.G * sizeof(int32_t), stream, a);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    hipLaunchKernelGGL(moe_sort_kernel, dim3((unsigned)groups), dim3(kSortThreads),
+                       p.G * (3 * sizeof(int32_t) + kSortWaves * sizeof(uint16_t)), stream, a);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- dispatch, by token
+
+struct DispatchArgs {
+    const void *x;
+    const float *weights;         // [T][top_k] or NULL
+    const int32_t *rows;          // [T][top_k]
+    const uint16_t *ye;           // kDot: the experts' outputs [R][K]
+    float *dw;                    // kDot: [T][top_k]
+    uint16_t *y;
+    uint8_t *q;
+    void *sf;
+    int64_t ld_x, sf_group;       // sf words of one group
+    int T, top_k, K, R, cap, ld_sf, format;
+};
+
+// A token's row is read once, quantised (once without weights) and written to
+// each of its rows.  Columns and lanes as in the norms: WPR waves share a
+// token (WPR = 1: four tokens per workgroup), lane l of wave w holds the 8
+// columns from 8 * (64 * (WPR * c + w) + l).  Neighbouring tokens run on one
+// XCD and have neighbouring rows in each expert, so that the scales, 4 bytes a
+// row and block, meet in one L2's lines.
+// With weights, the block's maximum is |w| max|x|: rounding is monotone, so
+// that is the largest of the rounded products.
+// kDot: also dw[t, j] = x[t] . ye[rows[t, j]], added up in a fixed order.
+template <typename TX, int WPR, int NCH, bool kW, bool kDot>
+__global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR)
+moe_dispatch_kernel(DispatchArgs p) {
+    constexpr int kBatch = 8;                          // choices between two barriers of the dot products
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int blk = xcd_remap(blockIdx.x, gridDim.x);
+    const int tok = WPR == 1 ? blk * 4 + wave : blk;
+    const int w0 = WPR == 1 ? 0 : wave;
+    const int K = p.K, top_k = p.top_k;
+    if (WPR == 1 && tok >= p.T) return;
+    const int32_t *rows = p.rows + (int64_t)tok * top_k;
+    const float *ws = kW ? p.weights + (int64_t)tok * top_k : nullptr;
+
+    const TX *xr = static_cast<const TX *>(p.x) + (int64_t)tok * p.ld_x;
+    Raw8<TX> xv[NCH];
+    int col[NCH];
+    static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
+        constexpr int c = decltype(cc)::value;
+        col[c] = 8 * (64 * (WPR * c + w0) + lane);
+        xv[c] = load8<true>(xr + min(col[c], K - 8));
+    });
+    __shared__ float red[kDot ? kBatch : 1][kDot ? WPR : 1];
+    if constexpr (kDot) {
+        for (int j0 = 0; j0 < top_k; j0 += kBatch) {
+            static_for<kBatch>([&](auto jc) __attribute__((always_inline)) {
+                constexpr int j = decltype(jc)::value;
+                if (j0 + j < top_k) {                  // uniform
+                    const int r = rows[j0 + j];
+                    float d = 0.f;
+                    if ((unsigned)r < (unsigned)p.R) {
+                        const uint16_t *yr = p.ye + (int64_t)r * K;
+                        Raw8<uint16_t> yv[NCH];
+                        static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
+                            constexpr int c = decltype(cc)::value;
+                            yv[c] = load8<true>(yr + min(col[c], K - 8));
+                        });
+                        static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
+                            constexpr int c = decltype(cc)::value;
+                            if (col[c] < K) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) d = __builtin_fmaf(get8(xv[c], i), get8(yv[c], i), d);
+                            }
+                        });
+                        d = sum64(d);
+                    }
+                    if constexpr (WPR == 1) {
+                        if (lane == 0) p.dw[(int64_t)tok * top_k + j0 + j] = d;
+                    } else {
+                        if (lane == 0) red[j][w0] = d;
+                    }
+                }
+            });
+            if constexpr (WPR > 1) {
+                __syncthreads();
+                if (threadIdx.x < kBatch && j0 + (int)threadIdx.x < top_k) {
+                    float d = 0.f;
+#pragma unroll
+                    for (int i = 0; i < WPR; ++i) d += red[threadIdx.x][i];
+                    p.dw[(int64_t)tok * top_k + j0 + threadIdx.x] = d;
+                }
+                if (j0 + kBatch < top_k) __syncthreads();
+            }
+        }
+    }
+    if (!p.q && !p.y) return;                          // uniform
+    static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
+        constexpr int c = decltype(cc)::value;
+        const bool in = col[c] < K;
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = get8(xv[c], i);
+        const float amax = max16(amax8(x));
+        float s = 0.f;
+        uint2 code = uint2{0, 0};
+        uint32_t word = 0;
+        if constexpr (!kW) {
+            if (p.q) {
+                code = codes8(x, amax, p.format, s);
+                if (p.format == kSfPacked) word = scale_word(s, in, lane);
+            }
+        }
+        for (int j = 0; j < top_k; ++j) {
+            const int r = rows[j];                     // uniform
+            if ((unsigned)r >= (unsigned)p.R) continue;
+            float v[8];
+            if constexpr (kW) {
+                const float w = ws[j];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = w * x[i];
+                if (p.q) {
+                    code = codes8(v, fabsf(w) * amax, p.format, s);
+                    if (p.format == kSfPacked) word = scale_word(s, in, lane);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = x[i];
+            }
+            if (p.y && in) store8<true>(p.y + (int64_t)r * K + col[c], v);
+            if (p.q) {
+                if (in) *reinterpret_cast<uint2 *>(p.q + (int64_t)r * K + col[c]) = code;
+                const int g = r / p.cap;
+                const int64_t at = g * p.sf_group + (r - g * p.cap);
+                if (p.format == kSfPacked) {
+                    if (lane == 0 && in) static_cast<uint32_t *>(p.sf)[at + (int64_t)(WPR * c + w0) * p.ld_sf] = word;
+                } else if ((lane & 15) == 0 && in) {
+                    static_cast<float *>(p.sf)[at + (int64_t)(col[c] / kKBlock) * p.ld_sf] = s;
+                }
+            }
+        }
+    });
+}
+
+template <typename TX, int WPR, int NCH, bool kW, bool kDot>
+static hipError_t launch_dispatch_t(const DispatchArgs &a, hipStream_t stream) {
+    const int64_t groups = WPR == 1 ? ((int64_t)a.T + 3) / 4 : a.T;
+    constexpr int kThreads = WPR == 1 ? 256 : 64 * WPR;
+    if (!grid_fits(groups, kThreads)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((moe_dispatch_kernel<TX, WPR, NCH, kW, kDot>), dim3((unsigned)groups), dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <typename TX, bool kW, bool kDot>
+static hipError_t launch_dispatch_k(const DispatchArgs &a, hipStream_t stream) {
+    const int n = (a.K + 511) / 512;                   // 512-column chunks
+    if (n <= 1) return launch_dispatch_t<TX, 1, 1, kW, kDot>(a, stream);
+    if (n <= 2) return launch_dispatch_t<TX, 1, 2, kW, kDot>(a, stream);
+    if (n <= 4) return launch_dispatch_t<TX, 4, 1, kW, kDot>(a, stream);
+    if (n <= 16 && a.T < 512) return launch_dispatch_t<TX, 16, 1, kW, kDot>(a, stream);
+    if (n <= 8) return launch_dispatch_t<TX, 4, 2, kW, kDot>(a, stream);
+    if (n <= 16) return launch_dispatch_t<TX, 4, 4, kW, kDot>(a, stream);
+    if (n <= 32) return launch_dispatch_t<TX, 16, 2, kW, kDot>(a, stream);
+    return hipErrorInvalidValue;
+}
+
+template <typename TX>
+static hipError_t launch_dispatch_w(const DispatchArgs &a, hipStream_t stream) {
+    if (a.dw) return a.weights ? launch_dispatch_k<TX, true, true>(a, stream) : launch_dispatch_k<TX, false, true>(a, stream);
+    return a.weights ? launch_dispatch_k<TX, true, false>(a, stream) : launch_dispatch_k<TX, false, false>(a, stream);
+}
+
+// ---------------------------------------------------------------- dispatch, by 128 x 128 tile
+
+struct TileArgs {
+    const void *x;
+    const float *weights;
+    const int32_t *src;
+    uint16_t *y;
+    uint8_t *q;
+    void *sf;
+    uint8_t *qt;
+    float *sft;
+    int64_t ld_x;
+    int pairs, top_k, K, R, tiles_m;
+};
+
+// Both scale directions of a 128 x 128 tile of the experts' rows at once: 512
+// threads, thread t holds columns 8 (t % 16) .. +7 of rows t / 16 + 32 i
+// (i < 4), so 16 lanes hold a row's 128 columns (its scale is a reduction
+// inside the DPP row); the column maxima go through LDS.  Rows that hold no
+// pair are zeros; they are written in qt and left alone in q and y.
+// A token's row is read once per choice.  The tiles of one column run one after
+// the other on one XCD, so that all but the first read of a token's 128 columns
+// find them in its L2 (8192 tokens: 2 MB of 4).
+template <typename TX, int FMT>
+__global__ void __launch_bounds__(512, 4) moe_dispatch_tile_kernel(TileArgs p) {
+    constexpr bool UE = FMT != kSfFp32;
+    const int t = threadIdx.x;
+    const int c8 = 8 * (t & 15), rg = t >> 4;
+    const int tile = xcd_remap(blockIdx.x, gridDim.x);
+    const int tn = tile / p.tiles_m, tm = tile - tn * p.tiles_m;
+    const int K = p.K, n0 = tn * 128, m0 = tm * 128;
+    int pair[4];
+    float w[4];
+    Raw8<TX> raw[4];
+    static_for<4>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+        pair[i] = p.src[m0 + rg + 32 * i];             // R is a multiple of 128
+        if ((unsigned)pair[i] >= (unsigned)p.pairs) pair[i] = -1;
+    });
+    static_for<4>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+        raw[i] = Raw8<TX>{};
+        w[i] = 1.f;
+        if (pair[i] >= 0) {
+            raw[i] = load8(static_cast<const TX *>(p.x) + (int64_t)(pair[i] / p.top_k) * p.ld_x + n0 + c8);
+            if (p.weights) w[i] = p.weights[pair[i]];  // uniform
+        }
+    });
+    float v[4][8];
+    static_for<4>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+        const bool scaled = p.weights && pair[i] >= 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float f = get8(raw[i], e);
+            v[i][e] = scaled ? w[i] * f : f;
+        }
+    });
+    __shared__ __attribute__((aligned(16))) float wmax[32][128];
+    __shared__ __attribute__((aligned(16))) float div_y[128], div_s[128];
+    {
+        float m[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            m[e] = fmaxf(fmaxf(fabsf(v[0][e]), fabsf(v[1][e])), fmaxf(fabsf(v[2][e]), fabsf(v[3][e])));
+        store8(&wmax[rg][c8], m);
+    }
+    static_for<4>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+        const int64_t row = m0 + rg + 32 * i;
+        const bool live = pair[i] >= 0;
+        if (p.y && live) store8(p.y + row * K + n0 + c8, v[i]);
+        if (p.q) {                                     // uniform
+            float s;
+            const uint2 code = codes8(v[i], max16(amax8(v[i])), FMT, s);
+            if (live) {
+                *reinterpret_cast<uint2 *>(p.q + row * K + n0 + c8) = code;
+                if (c8 == 0)
+                    store_block_scale<FMT == kSfPacked>(static_cast<uint32_t *>(p.sf), p.R, row, tn, K / 128, s);
+            }
+        }
+    });
+    if (!p.qt) return;                                 // uniform
+    __syncthreads();
+    if (t < 128) {
+        float m = wmax[0][t];
+#pragma unroll
+        for (int r = 1; r < 32; ++r) m = fmaxf(m, wmax[r][t]);
+        const float s = block_scale<UE>(m);
+        const BlockDivisor d = block_divisor<UE>(s);
+        div_y[t] = d.y;
+        div_s[t] = d.s;
+        p.sft[(int64_t)tm * K + n0 + t] = s;
+    }
+    __syncthreads();
+    const Raw8<float> y = load8(&div_y[c8]), s = load8(&div_s[c8]);
+    static_for<4>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = divide<UE>(v[i][e], BlockDivisor{get8(y, e), get8(s, e)});
+        *reinterpret_cast<uint2 *>(p.qt + (int64_t)(m0 + rg + 32 * i) * K + n0 + c8) =
+            uint2{e4m3_encode4(z[0], z[1], z[2], z[3]), e4m3_encode4(z[4], z[5], z[6], z[7])};
+    });
+}
+
+template <typename TX>
+static hipError_t launch_tile(const TileArgs &a, int format, hipStream_t stream) {
+    const int64_t grid = (int64_t)a.tiles_m * (a.K / 128);
+    if (!grid_fits(grid, 512)) return hipErrorInvalidValue;
+    const dim3 g((unsigned)grid), b(512);
+    if (format == kSfFp32) hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfFp32>), g, b, 0, stream, a);
+    else if (format == kSfUe8m0) hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfUe8m0>), g, b, 0, stream, a);
+    else hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfPacked>), g, b, 0, stream, a);
+    return hipGetLastError();
+}
+
+// By tile where column-scaled codes are wanted (every output but dw then comes
+// from there), by token otherwise.
+hipError_t launch_moe_dispatch(const MoeDispatchProblem &p, hipStream_t stream) {
+    const bool tile = p.qt != nullptr && p.R > 0;
+    const bool token = p.T > 0 && (p.dw || (!tile && (p.q || p.y)));
+    if (token) {
+        const DispatchArgs a{p.x, p.weights, p.rows, p.ye, p.dw, tile ? nullptr : p.y, tile ? nullptr : p.q, p.sf, p.ld_x,
+                             p.sf_group, p.T, p.top_k, p.K, p.R, p.cap, p.ld_sf, p.format};
+        const hipError_t err = p.x_type == kBf16 ? launch_dispatch_w<uint16_t>(a, stream) : launch_dispatch_w<float>(a, stream);
+        if (err != hipSuccess) return err;
+    }
+    if (!tile) return hipSuccess;
+    const TileArgs a{p.x, p.weights, p.src, p.y, p.q, p.sf, p.qt, p.sft, p.ld_x, p.T * p.top_k, p.top_k, p.K, p.R, p.R / 128};
+    return p.x_type == kBf16 ? launch_tile<uint16_t>(a, p.format, stream) : launch_tile<float>(a, p.format, stream);
+}
+
+// ---------------------------------------------------------------- dispatch of codes
+
+struct CopyArgs {
+    const uint8_t *x;
+    const uint32_t *sf_in;
+    const int32_t *rows;
+    uint8_t *q;
+    uint32_t *sf;
+    int64_t sf_group;
+    int T, top_k, K, R, cap, ld_in, ld_sf, words;   // words of a token's scales
+};
+
+// A workgroup of 256 threads per token: its codes (16 per lane) and scales are
+// read once and written to each of its rows.
+__global__ void __launch_bounds__(256) moe_dispatch_codes_kernel(CopyArgs p) {
+    const int tok = xcd_remap(blockIdx.x, gridDim.x);
+    const int32_t *rows = p.rows + (int64_t)tok * p.top_k;
+    for (int c = threadIdx.x; c < p.K / 16; c += 256) {
+        const v4i v = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(p.x + (int64_t)tok * p.K) + c);
+        for (int j = 0; j < p.top_k; ++j) {
+            const int r = rows[j];
+            if ((unsigned)r < (unsigned)p.R) reinterpret_cast<v4i *>(p.q + (int64_t)r * p.K)[c] = v;
+        }
+    }
+    for (int b = threadIdx.x; b < p.words; b += 256) {
+        const uint32_t s = p.sf_in[(int64_t)b * p.ld_in + tok];
+        for (int j = 0; j < p.top_k; ++j) {
+            const int r = rows[j];
+            if ((unsigned)r >= (unsigned)p.R) continue;
+            const int g = r / p.cap;
+            p.sf[g * p.sf_group + (int64_t)b * p.ld_sf + (r - g * p.cap)] = s;
+        }
+    }
+}
+
+hipError_t launch_moe_dispatch_codes(const MoeCopyProblem &p, hipStream_t stream) {
+    if (!grid_fits(p.T, 256)) return hipErrorInvalidValue;
+    const CopyArgs a{p.x, p.sf_in, p.rows, p.q, p.sf, p.sf_group, p.T, p.top_k, p.K, p.R, p.cap, p.ld_in, p.ld_sf, p.words};
+    hipLaunchKernelGGL(moe_dispatch_codes_kernel, dim3((unsigned)p.T), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- combine
+
+struct CombineArgs {
+    const uint16_t *y;
+    const float *weights;
+    const int32_t *rows;
+    const void *res;
+    void *out;
+    int T, top_k, K, R, chunks;   // 512-column chunks of a row
+};
+
+// A wave per token and 512 columns (lane l: columns 8 l .. 8 l + 7 of them);
+// nothing is shared between waves, and the loads of eight choices are in flight
+// together.  The sum runs in the order of the choices, in fp32.
+template <typename TO, bool kRes, bool kW>
+__global__ void __launch_bounds__(256) moe_combine_kernel(CombineArgs p) {
+    constexpr int kBatch = 8;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t item = (int64_t)xcd_remap(blockIdx.x, gridDim.x) * 4 + wave;
+    const int64_t tok = item / p.chunks;
+    if (tok >= p.T) return;
+    const int K = p.K, top_k = p.top_k;
+    const int col = (int)(item - tok * p.chunks) * 512 + 8 * lane;
+    const bool in = col < K;
+    const int at = min(col, K - 8);
+    const int32_t *rows = p.rows + tok * top_k;
+    float acc[8];
+    if constexpr (kRes) {
+        const Raw8<TO> r = load8<true>(static_cast<const TO *>(p.res) + tok * K + at);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = get8(r, i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    }
+    for (int j0 = 0; j0 < top_k; j0 += kBatch) {
+        Raw8<uint16_t> v[kBatch];
+        bool live[kBatch];
+        float w[kBatch];
+        static_for<kBatch>([&](auto jc) __attribute__((always_inline)) {
+            constexpr int j = decltype(jc)::value;
+            live[j] = false;
+            if (j0 + j < top_k) {                      // uniform
+                const int r = rows[j0 + j];
+                live[j] = (unsigned)r < (unsigned)p.R;
+                if (live[j]) {
+                    v[j] = load8<true>(p.y + (int64_t)r * K + at);
+                    if constexpr (kW) w[j] = p.weights[tok * top_k + j0 + j];
+                }
+            }
+        });
+        static_for<kBatch>([&](auto jc) __attribute__((always_inline)) {
+            constexpr int j = decltype(jc)::value;
+            if (live[j]) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    acc[i] = kW ? __builtin_fmaf(w[j], get8(v[j], i), acc[i]) : acc[i] + get8(v[j], i);
+            }
+        });
+    }
+    if (in) store8<true>(static_cast<TO *>(p.out) + tok * K + col, acc);
+}
+
+template <typename TO>
+static hipError_t launch_combine_t(const CombineArgs &a, hipStream_t stream) {
+    const int64_t groups = ((int64_t)a.T * a.chunks + 3) / 4;
+    if (!grid_fits(groups, 256)) return hipErrorInvalidValue;
+    const dim3 g((unsigned)groups), b(256);
+    if (a.res) {
+        if (a.weights) hipLaunchKernelGGL((moe_combine_kernel<TO, true, true>), g, b, 0, stream, a);
+        else hipLaunchKernelGGL((moe_combine_kernel<TO, true, false>), g, b, 0, stream, a);
+    } else {
+        if (a.weights) hipLaunchKernelGGL((moe_combine_kernel<TO, false, true>), g, b, 0, stream, a);
+        else hipLaunchKernelGGL((moe_combine_kernel<TO, false, false>), g, b, 0, stream, a);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(const MoeCombineProblem &p, hipStream_t stream) {
+    const CombineArgs a{p.y, p.weights, p.rows, p.residual, p.out, p.T, p.top_k, p.K, p.R, (p.K + 511) / 512};
+    return p.out_type == kBf16 ? launch_combine_t<uint16_t>(a, stream) : launch_combine_t<float>(a, stream);
+}
+
+}  // namespace dg
