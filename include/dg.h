@@ -694,8 +694,8 @@ int64_t dg_get_layernorm_backward_workspace_size(int rows, int K);
  *   same results take longer where that is not 0.
  * A call with T = 0 writes the plan of no pairs.
  * Errors: DG_ERR_NULL (ids, rows with T > 0; masked_m); DG_ERR_SHAPE (T < 0,
- * top_k < 1, G < 1 or > 1024, M_total < 0 or % 128, M_cap < 1; T * top_k + 128 G
- * or the rows reaching 2^31); DG_ERR_ALIGN.
+ * top_k < 1, T * top_k > 2^26, G < 1 or > 1024, M_total < 0 or % 128, M_cap < 1;
+ * the rows reaching 2^31); DG_ERR_ALIGN.
  */
 int dg_moe_sort_contiguous(const int32_t *ids, int T, int top_k, int G,
                            int32_t *rows, int32_t *src, int32_t *m_indices, int32_t *counts, int32_t *ks,

@@ -913,8 +913,8 @@ def _sort_workspace(workspace, T, top_k, G, device):
         return workspace
     if workspace != "auto":
         raise ValueError(f"workspace {workspace!r}")
-    # up to 2^15 pairs are sorted without one: no call to ask
-    n = get_moe_sort_workspace_size(T, top_k, G) if T * top_k > 32768 else 0
+    # up to 2^14 pairs are sorted without one: no call to ask
+    n = get_moe_sort_workspace_size(T, top_k, G) if T * top_k > 16384 else 0
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 

@@ -81,6 +81,7 @@ hipError_t launch_layernorm_bwd(const LayerNormBwdProblem &p, int num_cus, hipSt
 // 128-row blocks (cap = 0) or of cap rows.  counts: pairs that have a row,
 // ks: padded sizes.
 constexpr int kMoeMaxExperts = 1024;
+constexpr int64_t kMoeMaxPairs = (int64_t)1 << 26;   // of a sort
 struct MoeSortProblem {
     const int32_t *ids;
     int32_t *rows, *src, *expert, *counts, *ks;
@@ -88,7 +89,7 @@ struct MoeSortProblem {
     size_t ws_bytes;
     int n, G, cap, R;
 };
-// Needs 1 <= G <= kMoeMaxExperts, n + 128 G and R below 2^31.
+// Needs 1 <= G <= kMoeMaxExperts, n <= kMoeMaxPairs, R below 2^31.
 size_t moe_sort_workspace(int64_t n, int G);
 hipError_t launch_moe_sort(const MoeSortProblem &p, hipStream_t stream);
 
@@ -109,7 +110,7 @@ struct MoeDispatchProblem {
     int T, top_k, K, R, cap, ld_sf, x_type, format;
 };
 // Needs K a multiple of 128 up to kNormMaxK; with qt one group, R a multiple of 128.
-hipError_t launch_moe_dispatch(const MoeDispatchProblem &p, hipStream_t stream);
+hipError_t launch_moe_dispatch(const MoeDispatchProblem &p, int num_cus, hipStream_t stream);
 
 struct MoeCopyProblem {
     const uint8_t *x;

@@ -168,13 +168,14 @@ int64_t moe_pairs(int T, int top_k) {
     return T < 0 || top_k < 1 || n >= kOffsetLimit ? -1 : n;
 }
 
+bool moe_sort_sizes(int64_t n, int G) { return n >= 0 && n <= dg::kMoeMaxPairs && G >= 1 && G <= dg::kMoeMaxExperts; }
+
 int64_t moe_rows(int64_t n, int G) { return (n + 127 * (n < G ? n : G)) / 128 * 128; }
 
 int moe_sort(const int32_t *ids, int T, int top_k, int G, int32_t *rows, int32_t *src, int32_t *expert, int32_t *counts,
              int32_t *ks, int cap, int64_t R, void *workspace, size_t bytes, void *stream) {
     const int64_t n = moe_pairs(T, top_k);
-    if (n < 0 || G < 1 || G > dg::kMoeMaxExperts || n + 128 * (int64_t)G >= kOffsetLimit || R < 0 || R >= kOffsetLimit)
-        return DG_ERR_SHAPE;
+    if (!moe_sort_sizes(n, G) || R < 0 || R >= kOffsetLimit) return DG_ERR_SHAPE;
     if (n > 0 && (!ids || !rows)) return DG_ERR_NULL;
     if (!aligned4(ids) || !aligned4(rows) || !aligned4(src) || !aligned16(expert) || !aligned4(counts) || !aligned4(ks) ||
         !aligned16(workspace))
@@ -219,7 +220,7 @@ int moe_dispatch(const void *x, int x_type, int64_t ld_x, const uint16_t *ye, co
     const int64_t words = format == dg::kSfPacked ? (K / 128 + 3) / 4 : K / 128;
     const dg::MoeDispatchProblem p{x, weights, rows, src, ye, o.dw, o.y, o.q, o.sf, o.qt, o.sft, ld_x, words * ld, T, top_k,
                                    K, (int)R, (int)cap, ld, x_type, format};
-    return status(dg::launch_moe_dispatch(p, static_cast<hipStream_t>(stream)));
+    return status(dg::launch_moe_dispatch(p, cus, static_cast<hipStream_t>(stream)));
 }
 
 int moe_contiguous(const void *x, int x_type, int64_t ld_x, const uint16_t *ye, const float *weights, const int32_t *rows,
@@ -425,13 +426,13 @@ int dg_layernorm_backward(const void *dy, int dy_type, const void *h, int h_type
 
 int64_t dg_get_moe_rows(int T, int top_k, int G) {
     const int64_t n = moe_pairs(T, top_k);
-    if (n < 0 || G < 1 || G > dg::kMoeMaxExperts || n + 128 * (int64_t)G >= kOffsetLimit) return DG_ERR_SHAPE;
+    if (!moe_sort_sizes(n, G)) return DG_ERR_SHAPE;
     return moe_rows(n, G);
 }
 
 int64_t dg_get_moe_sort_workspace_size(int T, int top_k, int G) {
     const int64_t n = moe_pairs(T, top_k);
-    if (n < 0 || G < 1 || G > dg::kMoeMaxExperts || n + 128 * (int64_t)G >= kOffsetLimit) return DG_ERR_SHAPE;
+    if (!moe_sort_sizes(n, G)) return DG_ERR_SHAPE;
     return (int64_t)dg::moe_sort_workspace(n, G);
 }
 

@@ -22,7 +22,7 @@ struct SortArgs {
     const int32_t *ids;
     int32_t *rows, *src, *expert, *counts, *ks;
     int32_t *hist;       // per workgroup and expert, from the counting kernel; NULL: counted here
-    int n, G, cap, R, chunk;
+    int n, G, cap, R, chunk, chunks;
 };
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_count_kernel(SortArgs p) {
     extern __shared__ int32_t bins[];
     for (int e = threadIdx.x; e < p.G; e += kSortThreads) bins[e] = 0;
     __syncthreads();
-    const int lo = blockIdx.x * p.chunk, hi = (int)min((int64_t)lo + p.chunk, (int64_t)p.n);
+    const int lo = blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.n);
     for (int i = lo + threadIdx.x; i < hi; i += kSortThreads) {
         const int e = p.ids[i];
         if ((unsigned)e < (unsigned)p.G) atomicAdd(&bins[e], 1);
@@ -61,34 +61,63 @@ __device__ __forceinline__ uint64_t same_key(int key, int bits) {
 // only count.
 //
 // LDS: before[G], total[G], start[G] (32 bits) and the waves' counts [16][G]
-// (16 bits: a chunk is at most 2^15 pairs).
+// (16 bits: a chunk is at most 2^13 pairs), whose place the counting of other
+// chunks uses first, four copies of each bin by lane so that a popular expert
+// holds a wave up a quarter as long.
 __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(SortArgs p) {
-    extern __shared__ int32_t lds[];
+    extern __shared__ __attribute__((aligned(16))) int32_t lds[];
     const int G = p.G, t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    int32_t *before = lds, *total = lds + G, *start = lds + 2 * G;
-    uint16_t *hist = reinterpret_cast<uint16_t *>(lds + 3 * G);
+    int32_t *bins = lds, *before = lds + 8 * G, *total = before + G, *start = total + G;
+    uint16_t *hist = reinterpret_cast<uint16_t *>(lds);
     __shared__ int32_t scan[kSortWaves];
-    for (int e = t; e < 3 * G; e += kSortThreads) lds[e] = 0;
-    for (int e = t; e < kSortWaves * G; e += kSortThreads) hist[e] = 0;
+    // workgroups past the last chunk rank nothing: they fill rows
+    const int lo = min((int)blockIdx.x * p.chunk, p.n), hi = min(lo + p.chunk, p.n);
+    const bool alone = gridDim.x == 1;
+    for (int e = t; e < 10 * G; e += kSortThreads) lds[e] = 0;
     __syncthreads();
-    const int lo = blockIdx.x * p.chunk, hi = (int)min((int64_t)lo + p.chunk, (int64_t)p.n);
     // ---- counts of the pairs before the chunk, and of those behind it
     if (p.hist) {
-        const int n = (int)gridDim.x;
-        for (int i = t; i < n * G; i += kSortThreads) {
-            const int b = i / G, e = i - b * G, c = p.hist[i];
-            if (c) atomicAdd(b < (int)blockIdx.x ? &before[e] : &total[e], b == (int)blockIdx.x ? 0 : c);
-        }
-    } else {
-        auto count = [&](int from, int to, int32_t *bins) __attribute__((always_inline)) {
-#pragma unroll 4
-            for (int i = from + t; i < to; i += kSortThreads) {
-                const int e = p.ids[i];
-                if ((unsigned)e < (unsigned)G) atomicAdd(&bins[e], 1);
+        const int parts = kSortThreads / G, part = t / G, e = t - part * G;      // G <= 1024
+        if (part < parts) {
+            int a = 0, b = 0;
+#pragma unroll 8
+            for (int c = part; c < p.chunks; c += parts) {
+                const int v = p.hist[(int64_t)c * G + e];
+                a += c < (int)blockIdx.x ? v : 0;
+                b += c > (int)blockIdx.x ? v : 0;
             }
-        };
-        count(0, lo, before);
-        count(hi, p.n, total);
+            atomicAdd(&before[e], a);
+            atomicAdd(&total[e], b);
+        }
+        __syncthreads();
+    } else if (!alone) {
+        constexpr int kLoads = 8;                      // in flight
+        const int copy = lane & 3;
+        for (int i0 = 0; i0 < p.n; i0 += kLoads * kSortThreads) {          // n <= 2^26
+            int e[kLoads];
+            static_for<kLoads>([&](auto uc) __attribute__((always_inline)) {
+                constexpr int u = decltype(uc)::value;
+                const int i = i0 + u * kSortThreads + t;
+                e[u] = i < p.n && (i < lo || i >= hi) ? p.ids[i] : -1;
+            });
+            static_for<kLoads>([&](auto uc) __attribute__((always_inline)) {
+                constexpr int u = decltype(uc)::value;
+                const bool behind = i0 + u * kSortThreads >= hi;    // chunks are whole rows of threads
+                if ((unsigned)e[u] < (unsigned)G) atomicAdd(&bins[(behind ? 4 * G : 0) + 4 * e[u] + copy], 1);
+            });
+        }
+        __syncthreads();
+        if (t < 2 * G) {
+            const v4i c = *reinterpret_cast<const v4i *>(bins + 4 * t);
+            before[t] = c.x + c.y + c.z + c.w;         // before[G], then total[G]
+        }
+        if (G > kSortThreads / 2 && t + kSortThreads < 2 * G) {
+            const v4i c = *reinterpret_cast<const v4i *>(bins + 4 * (t + kSortThreads));
+            before[t + kSortThreads] = c.x + c.y + c.z + c.w;
+        }
+        __syncthreads();
+        for (int e = t; e < 8 * G; e += kSortThreads) bins[e] = 0;
+        __syncthreads();
     }
     // ---- ranks within the wave's run
     constexpr int kMostRounds = 8;                     // chunk <= 8192
@@ -167,23 +196,32 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(SortArgs p) {
         }
     });
     // ---- this workgroup's share of the rows: the expert of each, and -1 where there is none
-    if (!p.src && !p.expert) return;
-    const int r_lo = (int)((int64_t)p.R * blockIdx.x / gridDim.x), r_hi = (int)((int64_t)p.R * (blockIdx.x + 1) / gridDim.x);
-    for (int r = r_lo + t; r < r_hi; r += kSortThreads) {
-        int a = 0;                                     // the last expert that starts at or before r
-        if (p.cap) {
-            a = r / p.cap;
-        } else {
-            int b = G;
-            while (b - a > 1) {
-                const int m = (a + b) >> 1;
-                if (start[m] <= r) a = m;
-                else b = m;
-            }
+    if (p.cap) {
+        if (!p.src) return;
+        const int r_lo = (int)((int64_t)p.R * blockIdx.x / gridDim.x), r_hi = (int)((int64_t)p.R * (blockIdx.x + 1) / gridDim.x);
+        for (int r = r_lo + t; r < r_hi; r += kSortThreads) {
+            const int e = r / p.cap;
+            if (r - e * p.cap >= total[e]) p.src[r] = -1;
         }
-        const bool held = r - start[a] < total[a];
-        if (p.expert) p.expert[r] = held ? a : -1;
-        if (p.src && !held) p.src[r] = -1;
+        return;
+    }
+    if (!p.src && !p.expert) return;
+    // a 128-row block per wave: all of it belongs to one segment, or to none
+    const int blocks = p.R / 128, step = (int)gridDim.x * kSortWaves;
+    for (int b = (int)blockIdx.x * kSortWaves + wave; b < blocks; b += step) {
+        int e = 0, top = G;                            // the last expert that starts at or before the block
+        while (top - e > 1) {
+            const int m = (e + top) >> 1;
+            if (start[m] <= 128 * b) e = m;
+            else top = m;
+        }
+        const int held = total[e] - (128 * b - start[e]);
+#pragma unroll
+        for (int h = 0; h < 128; h += 64) {
+            const bool in = h + lane < held;
+            if (p.expert) p.expert[128 * b + h + lane] = in ? e : -1;
+            if (p.src && !in) p.src[128 * b + h + lane] = -1;
+        }
     }
 }
 
@@ -195,29 +233,41 @@ static int sort_chunk(int64_t n) {
     return chunk;
 }
 
-constexpr int64_t kSortOneLaunch = 32768;
+// Most pairs for which every workgroup counts all of them instead of a kernel
+// before it (32768 pairs, 64 experts: 8.0 us with the kernel before it, 9.8 without;
+// 16384 pairs: 7.5 without; each in a graph).
+constexpr int64_t kSortOneLaunch = 16384;
+
+// Workgroups: one per chunk, and one per 2048 rows of m_indices and src to
+// fill (512 pairs on 256 experts, 33024 rows: 5.9 us, 15.9 with one
+// workgroup; 1998 pairs on 32: 5.7, 6.6 with one).
+constexpr int kSortFill = 2048;
+static int64_t sort_groups(int64_t n, int64_t R) {
+    const int chunk = sort_chunk(n);
+    const int64_t by_pairs = (n + chunk - 1) / chunk, by_rows = (R + kSortFill - 1) / kSortFill;
+    const int64_t g = by_rows < 64 ? by_rows : 64;
+    return by_pairs > g ? by_pairs : g > 0 ? g : 1;
+}
 
 size_t moe_sort_workspace(int64_t n, int G) {
     if (n <= kSortOneLaunch) return 0;
-    const int64_t groups = (n + sort_chunk(n) - 1) / sort_chunk(n);
-    return (size_t)groups * G * sizeof(int32_t);
+    return (size_t)((n + sort_chunk(n) - 1) / sort_chunk(n)) * G * sizeof(int32_t);
 }
 
 hipError_t launch_moe_sort(const MoeSortProblem &p, hipStream_t stream) {
     const int chunk = sort_chunk(p.n);
-    int64_t groups = ((int64_t)p.n + chunk - 1) / chunk;
-    if (groups < 1) groups = 1;                        // no pairs: the rows are filled all the same
+    const int64_t chunks = ((int64_t)p.n + chunk - 1) / chunk;
+    const int64_t groups = sort_groups(p.n, p.src || p.expert ? p.R : 0);
     if (!grid_fits(groups, kSortThreads)) return hipErrorInvalidValue;
     const size_t need = moe_sort_workspace(p.n, p.G);
-    SortArgs a{p.ids, p.rows, p.src, p.expert, p.counts, p.ks, nullptr, p.n, p.G, p.cap, p.R, chunk};
+    SortArgs a{p.ids, p.rows, p.src, p.expert, p.counts, p.ks, nullptr, p.n, p.G, p.cap, p.R, chunk, (int)chunks};
     if (need && p.ws && p.ws_bytes >= need) {
         a.hist = static_cast<int32_t *>(p.ws);
-        hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)groups), dim3(kSortThreads), p.G * sizeof(int32_t), stream, a);
+        hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)chunks), dim3(kSortThreads), p.G * sizeof(int32_t), stream, a);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
-    hipLaunchKernelGGL(moe_sort_kernel, dim3((unsigned)groups), dim3(kSortThreads),
-                       p.G * (3 * sizeof(int32_t) + kSortWaves * sizeof(uint16_t)), stream, a);
+    hipLaunchKernelGGL(moe_sort_kernel, dim3((unsigned)groups), dim3(kSortThreads), 11 * p.G * sizeof(int32_t), stream, a);
     return hipGetLastError();
 }
 
@@ -236,14 +286,41 @@ struct DispatchArgs {
     int T, top_k, K, R, cap, ld_sf, format;
 };
 
+// Sixteen consecutive values as stored.
+template <typename T>
+struct Raw16 {
+    Raw8<T> lo, hi;
+};
+template <typename T>
+__device__ __forceinline__ Raw16<T> load16(const T *p) {
+    return {load8<true>(p), load8<true>(p + 8)};
+}
+template <typename T>
+__device__ __forceinline__ float get16(const Raw16<T> &r, int i) {
+    return i < 8 ? get8(r.lo, i) : get8(r.hi, i - 8);
+}
+
+// The maximum over each 8 lanes (of a 128-column block), in all of them; NaN is left out.
+__device__ __forceinline__ float max_of_8_lanes(float x) {
+    auto moved = [&](auto ctrl) __attribute__((always_inline)) {
+        return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    x = fmaxf(x, moved(std::integral_constant<int, 0xb1>{}));     // quad_perm 1 0 3 2
+    x = fmaxf(x, moved(std::integral_constant<int, 0x4e>{}));     // quad_perm 2 3 0 1
+    return fmaxf(x, moved(std::integral_constant<int, 0x141>{})); // row_half_mirror
+}
+
 // A token's row is read once, quantised (once without weights) and written to
-// each of its rows.  Columns and lanes as in the norms: WPR waves share a
-// token (WPR = 1: four tokens per workgroup), lane l of wave w holds the 8
-// columns from 8 * (64 * (WPR * c + w) + l).  Neighbouring tokens run on one
-// XCD and have neighbouring rows in each expert, so that the scales, 4 bytes a
-// row and block, meet in one L2's lines.
+// each of its rows.  WPR waves share a token (WPR = 1: four tokens per
+// workgroup); lane l of wave w holds the 16 columns from
+// 16 * (64 * (WPR * c + w) + l), c < NCH, so 8 lanes hold a 128-column block and
+// a store writes 1 KB of a row's codes.  The blocks' maxima meet in LDS, from
+// where one store writes up to 64 scales of a row: each lies in a line of its
+// own, and neighbouring tokens, which run on one XCD, have neighbouring rows in
+// each expert, so that their scales fill these lines in one L2.
 // With weights, the block's maximum is |w| max|x|: rounding is monotone, so
 // that is the largest of the rounded products.
+// blockIdx.y: a share of the choices, where there are few tokens.
 // kDot: also dw[t, j] = x[t] . ye[rows[t, j]], added up in a fixed order.
 template <typename TX, int WPR, int NCH, bool kW, bool kDot>
 __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR)
@@ -254,45 +331,46 @@ moe_dispatch_kernel(DispatchArgs p) {
     const int blk = xcd_remap(blockIdx.x, gridDim.x);
     const int tok = WPR == 1 ? blk * 4 + wave : blk;
     const int w0 = WPR == 1 ? 0 : wave;
-    const int K = p.K, top_k = p.top_k;
+    const int K = p.K;
     if (WPR == 1 && tok >= p.T) return;
-    const int32_t *rows = p.rows + (int64_t)tok * top_k;
-    const float *ws = kW ? p.weights + (int64_t)tok * top_k : nullptr;
+    const int j_lo = p.top_k * (int)blockIdx.y / (int)gridDim.y, j_hi = p.top_k * ((int)blockIdx.y + 1) / (int)gridDim.y;
+    const int32_t *rows = p.rows + (int64_t)tok * p.top_k;
+    const float *ws = kW ? p.weights + (int64_t)tok * p.top_k : nullptr;
 
     const TX *xr = static_cast<const TX *>(p.x) + (int64_t)tok * p.ld_x;
-    Raw8<TX> xv[NCH];
+    Raw16<TX> xv[NCH];
     int col[NCH];
     static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
         constexpr int c = decltype(cc)::value;
-        col[c] = 8 * (64 * (WPR * c + w0) + lane);
-        xv[c] = load8<true>(xr + min(col[c], K - 8));
+        col[c] = 16 * (64 * (WPR * c + w0) + lane);
+        xv[c] = load16(xr + min(col[c], K - 16));
     });
-    __shared__ float red[kDot ? kBatch : 1][kDot ? WPR : 1];
     if constexpr (kDot) {
-        for (int j0 = 0; j0 < top_k; j0 += kBatch) {
+        __shared__ float red[kBatch][WPR];
+        for (int j0 = j_lo; j0 < j_hi; j0 += kBatch) {
             static_for<kBatch>([&](auto jc) __attribute__((always_inline)) {
                 constexpr int j = decltype(jc)::value;
-                if (j0 + j < top_k) {                  // uniform
+                if (j0 + j < j_hi) {                   // uniform
                     const int r = rows[j0 + j];
                     float d = 0.f;
                     if ((unsigned)r < (unsigned)p.R) {
                         const uint16_t *yr = p.ye + (int64_t)r * K;
-                        Raw8<uint16_t> yv[NCH];
+                        Raw16<uint16_t> yv[NCH];
                         static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
                             constexpr int c = decltype(cc)::value;
-                            yv[c] = load8<true>(yr + min(col[c], K - 8));
+                            yv[c] = load16(yr + min(col[c], K - 16));
                         });
                         static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
                             constexpr int c = decltype(cc)::value;
                             if (col[c] < K) {
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) d = __builtin_fmaf(get8(xv[c], i), get8(yv[c], i), d);
+                                for (int i = 0; i < 16; ++i) d = __builtin_fmaf(get16(xv[c], i), get16(yv[c], i), d);
                             }
                         });
                         d = sum64(d);
                     }
                     if constexpr (WPR == 1) {
-                        if (lane == 0) p.dw[(int64_t)tok * top_k + j0 + j] = d;
+                        if (lane == 0) p.dw[(int64_t)tok * p.top_k + j0 + j] = d;
                     } else {
                         if (lane == 0) red[j][w0] = d;
                     }
@@ -300,90 +378,133 @@ moe_dispatch_kernel(DispatchArgs p) {
             });
             if constexpr (WPR > 1) {
                 __syncthreads();
-                if (threadIdx.x < kBatch && j0 + (int)threadIdx.x < top_k) {
+                if (threadIdx.x < kBatch && j0 + (int)threadIdx.x < j_hi) {
                     float d = 0.f;
 #pragma unroll
                     for (int i = 0; i < WPR; ++i) d += red[threadIdx.x][i];
-                    p.dw[(int64_t)tok * top_k + j0 + threadIdx.x] = d;
+                    p.dw[(int64_t)tok * p.top_k + j0 + threadIdx.x] = d;
                 }
-                if (j0 + kBatch < top_k) __syncthreads();
+                __syncthreads();
             }
         }
     }
     if (!p.q && !p.y) return;                          // uniform
-    static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
-        constexpr int c = decltype(cc)::value;
-        const bool in = col[c] < K;
-        float x[8];
+    // ---- the blocks' maxima, in registers and LDS
+    __shared__ float maxima[WPR == 1 ? 4 : 1][8 * WPR * NCH];
+    float *bmax = maxima[WPR == 1 ? wave : 0];
+    float amax[NCH];
+    uint4 code[NCH];
+    auto encode = [&](int c, float w, float m) __attribute__((always_inline)) {
+        float v[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = get8(xv[c], i);
-        const float amax = max16(amax8(x));
-        float s = 0.f;
-        uint2 code = uint2{0, 0};
-        uint32_t word = 0;
-        if constexpr (!kW) {
+        for (int i = 0; i < 16; ++i) v[i] = kW ? w * get16(xv[c], i) : get16(xv[c], i);
+        uint32_t o[4];
+        auto four = [&](auto ue) __attribute__((always_inline)) {
+            constexpr bool UE = decltype(ue)::value;
+            const BlockDivisor d = block_divisor<UE>(block_scale<UE>(m));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = encode4<UE>(v4f{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]}, d);
+        };
+        if (p.format == kSfFp32) four(std::false_type{});
+        else four(std::true_type{});
+        return uint4{o[0], o[1], o[2], o[3]};
+    };
+    if (p.q) {
+        static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
+            constexpr int c = decltype(cc)::value;
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(get16(xv[c], i)));
+            amax[c] = max_of_8_lanes(m);
+            if ((lane & 7) == 0) bmax[8 * (WPR * c + w0) + (lane >> 3)] = amax[c];
+            if constexpr (!kW) code[c] = encode(c, 1.f, amax[c]);
+        });
+        if constexpr (WPR > 1) __syncthreads();
+        else __builtin_amdgcn_wave_barrier();          // one wave's LDS accesses stay in order
+    }
+    // ---- the rows
+    for (int j = j_lo; j < j_hi; ++j) {
+        const int r = rows[j];                         // uniform
+        if ((unsigned)r >= (unsigned)p.R) continue;
+        const float w = kW ? ws[j] : 1.f;
+        static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
+            constexpr int c = decltype(cc)::value;
             if (p.q) {
-                code = codes8(x, amax, p.format, s);
-                if (p.format == kSfPacked) word = scale_word(s, in, lane);
+                if constexpr (kW) code[c] = encode(c, w, fabsf(w) * amax[c]);
+                if (col[c] < K)
+                    __builtin_nontemporal_store(__builtin_bit_cast(v4i, code[c]),
+                                                reinterpret_cast<v4i *>(p.q + (int64_t)r * K + col[c]));
             }
-        }
-        for (int j = 0; j < top_k; ++j) {
-            const int r = rows[j];                     // uniform
-            if ((unsigned)r >= (unsigned)p.R) continue;
-            float v[8];
-            if constexpr (kW) {
-                const float w = ws[j];
+            if (p.y && col[c] < K) {
+                float lo[8], hi[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = w * x[i];
-                if (p.q) {
-                    code = codes8(v, fabsf(w) * amax, p.format, s);
-                    if (p.format == kSfPacked) word = scale_word(s, in, lane);
+                for (int i = 0; i < 8; ++i) {
+                    lo[i] = kW ? w * get16(xv[c], i) : get16(xv[c], i);
+                    hi[i] = kW ? w * get16(xv[c], i + 8) : get16(xv[c], i + 8);
                 }
+                uint16_t *dst = p.y + (int64_t)r * K + col[c];
+                store8<true>(dst, lo);
+                store8<true>(dst + 8, hi);
+            }
+        });
+    }
+    if (!p.q) return;
+    // ---- their scales, a row per wave at a time
+    const int blocks = K / kKBlock, words = p.format == kSfPacked ? (blocks + 3) / 4 : blocks;
+    for (int j = j_lo + w0; j < j_hi; j += WPR) {
+        const int r = rows[j];
+        if ((unsigned)r >= (unsigned)p.R) continue;
+        const float w = kW ? fabsf(ws[j]) : 1.f;
+        const int g = p.cap == p.R ? 0 : r / p.cap;
+        uint32_t *sf = static_cast<uint32_t *>(p.sf) + g * p.sf_group + (r - g * p.cap);
+        for (int b = lane; b < words; b += 64) {
+            uint32_t word;
+            if (p.format == kSfPacked) {
+                word = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (4 * b + i < blocks)
+                        word |= (__float_as_uint(block_scale<true>(kW ? w * bmax[4 * b + i] : bmax[4 * b + i])) >> 23) << (8 * i);
             } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = x[i];
+                const float m = kW ? w * bmax[b] : bmax[b];
+                word = __float_as_uint(p.format == kSfFp32 ? block_scale<false>(m) : block_scale<true>(m));
             }
-            if (p.y && in) store8<true>(p.y + (int64_t)r * K + col[c], v);
-            if (p.q) {
-                if (in) *reinterpret_cast<uint2 *>(p.q + (int64_t)r * K + col[c]) = code;
-                const int g = r / p.cap;
-                const int64_t at = g * p.sf_group + (r - g * p.cap);
-                if (p.format == kSfPacked) {
-                    if (lane == 0 && in) static_cast<uint32_t *>(p.sf)[at + (int64_t)(WPR * c + w0) * p.ld_sf] = word;
-                } else if ((lane & 15) == 0 && in) {
-                    static_cast<float *>(p.sf)[at + (int64_t)(col[c] / kKBlock) * p.ld_sf] = s;
-                }
-            }
+            sf[(int64_t)b * p.ld_sf] = word;
         }
-    });
+    }
 }
 
 template <typename TX, int WPR, int NCH, bool kW, bool kDot>
-static hipError_t launch_dispatch_t(const DispatchArgs &a, hipStream_t stream) {
+static hipError_t launch_dispatch_t(const DispatchArgs &a, int num_cus, hipStream_t stream) {
     const int64_t groups = WPR == 1 ? ((int64_t)a.T + 3) / 4 : a.T;
     constexpr int kThreads = WPR == 1 ? 256 : 64 * WPR;
-    if (!grid_fits(groups, kThreads)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((moe_dispatch_kernel<TX, WPR, NCH, kW, kDot>), dim3((unsigned)groups), dim3(kThreads), 0, stream, a);
+    // few tokens: the choices of one are dealt to several workgroups
+    const int64_t share = groups < num_cus ? (num_cus / groups < a.top_k ? num_cus / groups : a.top_k) : 1;
+    if (!grid_fits(groups * share, kThreads)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((moe_dispatch_kernel<TX, WPR, NCH, kW, kDot>), dim3((unsigned)groups, (unsigned)share), dim3(kThreads), 0,
+                       stream, a);
     return hipGetLastError();
 }
 
 template <typename TX, bool kW, bool kDot>
-static hipError_t launch_dispatch_k(const DispatchArgs &a, hipStream_t stream) {
-    const int n = (a.K + 511) / 512;                   // 512-column chunks
-    if (n <= 1) return launch_dispatch_t<TX, 1, 1, kW, kDot>(a, stream);
-    if (n <= 2) return launch_dispatch_t<TX, 1, 2, kW, kDot>(a, stream);
-    if (n <= 4) return launch_dispatch_t<TX, 4, 1, kW, kDot>(a, stream);
-    if (n <= 16 && a.T < 512) return launch_dispatch_t<TX, 16, 1, kW, kDot>(a, stream);
-    if (n <= 8) return launch_dispatch_t<TX, 4, 2, kW, kDot>(a, stream);
-    if (n <= 16) return launch_dispatch_t<TX, 4, 4, kW, kDot>(a, stream);
-    if (n <= 32) return launch_dispatch_t<TX, 16, 2, kW, kDot>(a, stream);
+static hipError_t launch_dispatch_k(const DispatchArgs &a, int num_cus, hipStream_t stream) {
+    const int n = (a.K + 1023) / 1024;                 // 1024-column chunks
+    if (n <= 1) return launch_dispatch_t<TX, 1, 1, kW, kDot>(a, num_cus, stream);
+    if (n <= 2) return launch_dispatch_t<TX, 2, 1, kW, kDot>(a, num_cus, stream);
+    if (n <= 4) return launch_dispatch_t<TX, 4, 1, kW, kDot>(a, num_cus, stream);
+    if (n <= 8 && a.T < 512) return launch_dispatch_t<TX, 8, 1, kW, kDot>(a, num_cus, stream);
+    if (n <= 8) return launch_dispatch_t<TX, 4, 2, kW, kDot>(a, num_cus, stream);
+    if (n <= 16) return launch_dispatch_t<TX, 8, 2, kW, kDot>(a, num_cus, stream);
     return hipErrorInvalidValue;
 }
 
 template <typename TX>
-static hipError_t launch_dispatch_w(const DispatchArgs &a, hipStream_t stream) {
-    if (a.dw) return a.weights ? launch_dispatch_k<TX, true, true>(a, stream) : launch_dispatch_k<TX, false, true>(a, stream);
-    return a.weights ? launch_dispatch_k<TX, true, false>(a, stream) : launch_dispatch_k<TX, false, false>(a, stream);
+static hipError_t launch_dispatch_w(const DispatchArgs &a, int num_cus, hipStream_t stream) {
+    if (a.dw)
+        return a.weights ? launch_dispatch_k<TX, true, true>(a, num_cus, stream)
+                         : launch_dispatch_k<TX, false, true>(a, num_cus, stream);
+    return a.weights ? launch_dispatch_k<TX, true, false>(a, num_cus, stream)
+                     : launch_dispatch_k<TX, false, false>(a, num_cus, stream);
 }
 
 // ---------------------------------------------------------------- dispatch, by 128 x 128 tile
@@ -505,13 +626,14 @@ static hipError_t launch_tile(const TileArgs &a, int format, hipStream_t stream)
 
 // By tile where column-scaled codes are wanted (every output but dw then comes
 // from there), by token otherwise.
-hipError_t launch_moe_dispatch(const MoeDispatchProblem &p, hipStream_t stream) {
+hipError_t launch_moe_dispatch(const MoeDispatchProblem &p, int num_cus, hipStream_t stream) {
     const bool tile = p.qt != nullptr && p.R > 0;
     const bool token = p.T > 0 && (p.dw || (!tile && (p.q || p.y)));
     if (token) {
         const DispatchArgs a{p.x, p.weights, p.rows, p.ye, p.dw, tile ? nullptr : p.y, tile ? nullptr : p.q, p.sf, p.ld_x,
                              p.sf_group, p.T, p.top_k, p.K, p.R, p.cap, p.ld_sf, p.format};
-        const hipError_t err = p.x_type == kBf16 ? launch_dispatch_w<uint16_t>(a, stream) : launch_dispatch_w<float>(a, stream);
+        const hipError_t err = p.x_type == kBf16 ? launch_dispatch_w<uint16_t>(a, num_cus, stream)
+                                                 : launch_dispatch_w<float>(a, num_cus, stream);
         if (err != hipSuccess) return err;
     }
     if (!tile) return hipSuccess;

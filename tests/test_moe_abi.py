@@ -79,7 +79,7 @@ def test_sort(lib):
               Call(lib.dg_moe_sort_masked, **common, masked_m=P, M_cap=4, workspace=P, workspace_bytes=0, stream=None)):
         for name in ("ids", "rows"):
             c.refuses(NULL, **{name: None})
-        for kw in (dict(T=-1), dict(top_k=0), dict(G=0), dict(G=1025), dict(T=BIG, top_k=2), dict(T=BIG - 1, top_k=2),
+        for kw in (dict(T=-1), dict(top_k=0), dict(G=0), dict(G=1025), dict(T=BIG, top_k=2), dict(T=1 << 25, top_k=3),
                    dict(T=(1 << 31) - 1, top_k=(1 << 31) - 1)):
             c.refuses(SHAPE, **kw)
         for name in ("ids", "rows", "src"):
@@ -101,14 +101,14 @@ def test_sort(lib):
 def test_sort_sizes(lib):
     rows, ws = lib.dg_get_moe_rows, lib.dg_get_moe_sort_workspace_size
     for f in (rows, ws):
-        for args in ((-1, 2, 8), (5, 0, 8), (5, 2, 0), (5, 2, 1025), (BIG, 2, 8)):
+        for args in ((-1, 2, 8), (5, 0, 8), (5, 2, 0), (5, 2, 1025), (BIG, 2, 8), ((1 << 26) + 1, 1, 8)):
             assert f(*args) == SHAPE, args
     assert rows(0, 2, 8) == 0 and rows(1, 1, 8) == 128 and rows(1, 8, 64) == 1024 and rows(128, 1, 1) == 128
     # whatever the counts, they fit: `used` experts of 128 b + 1 pairs each are the worst, and what is left fills up
     for n, G in ((1, 1), (127, 3), (129, 2), (1000, 7), (300, 300), (300, 299), (4097, 33)):
         worst = max(128 * (used + (n - used) // 128) for used in range(1, min(n, G) + 1))
         assert worst <= rows(n, 1, G) <= n + 127 * min(n, G), (n, G)
-    assert ws(4096, 8, 64) == 0
+    assert ws(2048, 8, 64) == 0 and ws(2049, 8, 64) == 17 * 64 * 4
 
 
 def dispatch_calls(lib, form):
