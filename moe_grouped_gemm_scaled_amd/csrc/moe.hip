@@ -519,78 +519,228 @@ struct TileArgs {
     uint8_t *qt;
     float *sft;
     int64_t ld_x;
-    int pairs, top_k, K, R, tiles_m;
+    int pairs, K, R, tiles_m;
+    uint32_t mul;      // pair / top_k = (pair * mul) >> (31 + shift), exactly for pair < 2^31
+    int shift;
 };
+
+// Magnitudes as integers, whose order is that of the numbers, with infinities
+// and then NaN on top: no canonicalisation, no separate test for NaN.  bf16:
+// two to a register.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+template <typename T>
+struct Mag8;   // magnitudes of 8 values, elementwise maxima of them, and their largest as fp32 bits
+template <>
+struct Mag8<uint16_t> {
+    uint32_t m[4];
+    __device__ __forceinline__ explicit Mag8(const Raw8<uint16_t> &r) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = (uint32_t)r.a[i] & 0x7fff7fffu;
+    }
+    __device__ __forceinline__ void max(const Mag8 &o) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = max_u16x2(m[i], o.m[i]);
+    }
+    __device__ __forceinline__ uint32_t largest() const {
+        const uint32_t v = max_u16x2(max_u16x2(m[0], m[1]), max_u16x2(m[2], m[3]));
+        return ::max(v & 0xffff0000u, v << 16);
+    }
+};
+template <>
+struct Mag8<float> {
+    uint32_t m[8];
+    __device__ __forceinline__ explicit Mag8(const Raw8<float> &r) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = __float_as_uint(get8(r, i)) & 0x7fffffffu;
+    }
+    __device__ __forceinline__ void max(const Mag8 &o) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = ::max(m[i], o.m[i]);
+    }
+    __device__ __forceinline__ uint32_t largest() const {
+        return ::max(::max(::max(m[0], m[1]), ::max(m[2], m[3])), ::max(::max(m[4], m[5]), ::max(m[6], m[7])));
+    }
+};
+template <int N>
+__device__ __forceinline__ uint32_t ror16u(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x120 + N, 0xf, 0xf, true);
+}
+__device__ __forceinline__ uint32_t max16u(uint32_t x) {
+    x = max(x, ror16u<8>(x));
+    x = max(x, ror16u<4>(x));
+    x = max(x, ror16u<2>(x));
+    return max(x, ror16u<1>(x));
+}
+// lane I of each four, in all of them
+template <int I>
+__device__ __forceinline__ float of_quad(float x) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), I * 0x55, 0xf, 0xf, true));
+}
+
+typedef unsigned Codes __attribute__((ext_vector_type(2)));   // of eight values
+
+// Four quotients as codes where none is NaN.
+__device__ __forceinline__ uint32_t e4m3_encode4_numbers(float a, float b, float c, float d) {
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
 
 // Both scale directions of a 128 x 128 tile of the experts' rows at once: 512
 // threads, thread t holds columns 8 (t % 16) .. +7 of rows t / 16 + 32 i
 // (i < 4), so 16 lanes hold a row's 128 columns (its scale is a reduction
 // inside the DPP row); the column maxima go through LDS.  Rows that hold no
 // pair are zeros; they are written in qt and left alone in q and y.
+//
 // A token's row is read once per choice.  The tiles of one column run one after
 // the other on one XCD, so that all but the first read of a token's 128 columns
-// find them in its L2 (8192 tokens: 2 MB of 4).
-template <typename TX, int FMT>
+// find them in its L2 (8192 tokens: 2 MB of 4; 118 MB read of HBM for 117 MB of
+// tokens, top_k = 4).
+//
+// Two codes per element are nearly as much arithmetic as the stores are time
+// (34500 rows of 7168, 8192 tokens, bf16: the loads and stores alone 133 us, the
+// arithmetic without the stores 80 us), so it is kept short: maxima of
+// magnitudes as integers, two bf16 at a time; of a row's 16 lanes, lane i % 4
+// works out row i's scale and divisor and hands them round by DPP; codes without
+// the NaN rule, which can only matter to a wave that has seen an infinity or NaN
+// (or a weight that makes one) and takes the general path.  Buffer stores keep
+// the addresses in scalar registers, which leaves room for four workgroups on a
+// CU (64 registers at most for bf16).  166 us, with weights 165; 192 and 203 with
+// the general arithmetic and addresses throughout; a fixed grid that fetches the
+// next tile ahead needs 80 to 97 registers and takes 190.
+template <typename TX, int FMT, bool kW>
 __global__ void __launch_bounds__(512, 4) moe_dispatch_tile_kernel(TileArgs p) {
     constexpr bool UE = FMT != kSfFp32;
+    constexpr uint32_t kInf = 0x7f800000u;
     const int t = threadIdx.x;
     const int c8 = 8 * (t & 15), rg = t >> 4;
     const int tile = xcd_remap(blockIdx.x, gridDim.x);
     const int tn = tile / p.tiles_m, tm = tile - tn * p.tiles_m;
     const int K = p.K, n0 = tn * 128, m0 = tm * 128;
-    int pair[4];
-    float w[4];
-    Raw8<TX> raw[4];
-    static_for<4>([&](auto ic) __attribute__((always_inline)) {
-        constexpr int i = decltype(ic)::value;
-        pair[i] = p.src[m0 + rg + 32 * i];             // R is a multiple of 128
-        if ((unsigned)pair[i] >= (unsigned)p.pairs) pair[i] = -1;
-    });
-    static_for<4>([&](auto ic) __attribute__((always_inline)) {
-        constexpr int i = decltype(ic)::value;
-        raw[i] = Raw8<TX>{};
-        w[i] = 1.f;
-        if (pair[i] >= 0) {
-            raw[i] = load8(static_cast<const TX *>(p.x) + (int64_t)(pair[i] / p.top_k) * p.ld_x + n0 + c8);
-            if (p.weights) w[i] = p.weights[pair[i]];  // uniform
-        }
-    });
-    float v[4][8];
-    static_for<4>([&](auto ic) __attribute__((always_inline)) {
-        constexpr int i = decltype(ic)::value;
-        const bool scaled = p.weights && pair[i] >= 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float f = get8(raw[i], e);
-            v[i][e] = scaled ? w[i] * f : f;
-        }
-    });
     __shared__ __attribute__((aligned(16))) float wmax[32][128];
     __shared__ __attribute__((aligned(16))) float div_y[128], div_s[128];
+    __shared__ int odd;                                // a wave has seen an infinity or NaN
+    if (t == 0) odd = 0;
+    uint32_t held = 0;                                 // bit i: row i holds a pair
+    float w[4];
+    Raw8<TX> raw[4];
     {
+        int pair[4];
+        static_for<4>([&](auto ic) __attribute__((always_inline)) {
+            constexpr int i = decltype(ic)::value;
+            pair[i] = p.src[m0 + rg + 32 * i];         // R is a multiple of 128
+        });
+        static_for<4>([&](auto ic) __attribute__((always_inline)) {
+            constexpr int i = decltype(ic)::value;
+            raw[i] = Raw8<TX>{};
+            w[i] = 0.f;
+            if ((unsigned)pair[i] < (unsigned)p.pairs) {
+                held |= 1u << i;
+                const int64_t tok = (int64_t)(((uint64_t)(uint32_t)pair[i] * p.mul) >> (31 + p.shift));
+                raw[i] = load8(static_cast<const TX *>(p.x) + tok * p.ld_x + n0 + c8);
+                if constexpr (kW) w[i] = p.weights[pair[i]];
+            }
+        });
+    }
+    auto value = [&](int i, int e) __attribute__((always_inline)) {
+        return kW ? w[i] * get8(raw[i], e) : get8(raw[i], e);
+    };
+    // ---- magnitudes: of the rows (over 16 lanes), and of the columns over the thread's four rows
+    uint32_t top[4];
+    bool strange = false;
+    {
+        Mag8<TX> cols(raw[0]);
+        static_for<4>([&](auto ic) __attribute__((always_inline)) {
+            constexpr int i = decltype(ic)::value;
+            const Mag8<TX> m(raw[i]);
+            top[i] = max16u(m.largest());
+            strange = strange || top[i] >= kInf;
+            if constexpr (kW) {
+                // rounding is monotone: the largest product is that of the largest magnitude
+                top[i] = __float_as_uint(fabsf(w[i]) * __uint_as_float(top[i]));
+                strange = strange || top[i] >= kInf || !(fabsf(w[i]) < __builtin_inff());
+            } else {
+                if constexpr (i > 0) cols.max(m);
+            }
+        });
+        strange = __any(strange);                      // uniform
         float m[8];
+        if (kW || strange) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            m[e] = fmaxf(fmaxf(fabsf(v[0][e]), fabsf(v[1][e])), fmaxf(fabsf(v[2][e]), fabsf(v[3][e])));
+            for (int e = 0; e < 8; ++e)                // fmaxf leaves NaN out
+                m[e] = fmaxf(fmaxf(fabsf(value(0, e)), fabsf(value(1, e))), fmaxf(fabsf(value(2, e)), fabsf(value(3, e))));
+        } else if constexpr (std::is_same<TX, float>::value) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m[e] = __uint_as_float(cols.m[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m[e] = __uint_as_float(e & 1 ? cols.m[e / 2] & 0xffff0000u : cols.m[e / 2] << 16);
+        }
         store8(&wmax[rg][c8], m);
     }
-    static_for<4>([&](auto ic) __attribute__((always_inline)) {
-        constexpr int i = decltype(ic)::value;
-        const int64_t row = m0 + rg + 32 * i;
-        const bool live = pair[i] >= 0;
-        if (p.y && live) store8(p.y + row * K + n0 + c8, v[i]);
-        if (p.q) {                                     // uniform
-            float s;
-            const uint2 code = codes8(v[i], max16(amax8(v[i])), FMT, s);
-            if (live) {
-                *reinterpret_cast<uint2 *>(p.q + row * K + n0 + c8) = code;
-                if (c8 == 0)
-                    store_block_scale<FMT == kSfPacked>(static_cast<uint32_t *>(p.sf), p.R, row, tn, K / 128, s);
-            }
-        }
-    });
+    if (strange) {
+        static_for<4>([&](auto ic) __attribute__((always_inline)) {
+            constexpr int i = decltype(ic)::value;
+            float m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(value(i, e)));
+            top[i] = __float_as_uint(max16(m));
+        });
+    }
+    auto codes = [&](int i, auto general, auto &&div) __attribute__((always_inline)) {
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = divide<UE>(value(i, e), div(e));
+        if constexpr (decltype(general)::value)
+            return Codes{e4m3_encode4(z[0], z[1], z[2], z[3]), e4m3_encode4(z[4], z[5], z[6], z[7])};
+        return Codes{e4m3_encode4_numbers(z[0], z[1], z[2], z[3]), e4m3_encode4_numbers(z[4], z[5], z[6], z[7])};
+    };
+    // The tile's window of a row-major tensor; row i of the thread lies 32 * i * K
+    // elements (a scalar) past its first, and an offset past the window drops
+    // the store of a row without a pair.
+    auto window = [&](const void *base, int size) __attribute__((always_inline)) {
+        return __builtin_amdgcn_make_buffer_rsrc((void *)((const char *)base + ((int64_t)m0 * K + n0) * size), (short)0,
+                                                 128 * K * size, 0x00020000);
+    };
+    const int at = rg * K + c8;
+    constexpr int kPast = 0x7ffffff0, kNt = 2;
+    // ---- the rows
+    if (p.y) {                                         // uniform
+        const __amdgpu_buffer_rsrc_t r = window(p.y, 2);
+        static_for<4>([&](auto ic) __attribute__((always_inline)) {
+            constexpr int i = decltype(ic)::value;
+            const v4i o = v4i{(int)pack_bf16x2_rne(value(i, 0), value(i, 1)), (int)pack_bf16x2_rne(value(i, 2), value(i, 3)),
+                              (int)pack_bf16x2_rne(value(i, 4), value(i, 5)), (int)pack_bf16x2_rne(value(i, 6), value(i, 7))};
+            __builtin_amdgcn_raw_buffer_store_b128(o, r, held & (1u << i) ? 2 * at : kPast, 64 * i * K, kNt);
+        });
+    }
+    if (p.q) {                                         // uniform
+        const __amdgpu_buffer_rsrc_t r = window(p.q, 1);
+        const int mine = t & 3;
+        const float amax = __uint_as_float(mine & 2 ? (mine & 1 ? top[3] : top[2]) : (mine & 1 ? top[1] : top[0]));
+        const float s = block_scale<UE>(amax);
+        const BlockDivisor d = block_divisor<UE>(s);
+        // lane i of the row's 16 stores row i's scale
+        if ((t & 15) < 4 && (held >> mine & 1))
+            store_block_scale<FMT == kSfPacked>(static_cast<uint32_t *>(p.sf), p.R, (int64_t)m0 + rg + 32 * mine, tn, K / 128, s);
+        auto out = [&](auto general) __attribute__((always_inline)) {
+            static_for<4>([&](auto ic) __attribute__((always_inline)) {
+                constexpr int i = decltype(ic)::value;
+                const BlockDivisor di{of_quad<i>(d.y), UE ? 0.f : of_quad<i>(d.s)};
+                __builtin_amdgcn_raw_buffer_store_b64(codes(i, general, [&](int) { return di; }), r,
+                                                      held & (1u << i) ? at : kPast, 32 * i * K, kNt);
+                __builtin_amdgcn_sched_barrier(0);     // row by row: interleaved rows need more registers
+            });
+        };
+        if (strange) out(std::true_type{});
+        else out(std::false_type{});
+    }
     if (!p.qt) return;                                 // uniform
-    __syncthreads();
+    // ---- the columns
+    __syncthreads();                                   // wmax, and odd is 0
+    if (strange && (t & 63) == 0) odd = 1;
     if (t < 128) {
         float m = wmax[0][t];
 #pragma unroll
@@ -602,26 +752,42 @@ __global__ void __launch_bounds__(512, 4) moe_dispatch_tile_kernel(TileArgs p) {
         p.sft[(int64_t)tm * K + n0 + t] = s;
     }
     __syncthreads();
+    const __amdgpu_buffer_rsrc_t r = window(p.qt, 1);
     const Raw8<float> y = load8(&div_y[c8]), s = load8(&div_s[c8]);
-    static_for<4>([&](auto ic) __attribute__((always_inline)) {
-        constexpr int i = decltype(ic)::value;
-        float z[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = divide<UE>(v[i][e], BlockDivisor{get8(y, e), get8(s, e)});
-        *reinterpret_cast<uint2 *>(p.qt + (int64_t)(m0 + rg + 32 * i) * K + n0 + c8) =
-            uint2{e4m3_encode4(z[0], z[1], z[2], z[3]), e4m3_encode4(z[4], z[5], z[6], z[7])};
-    });
+    auto out = [&](auto general) __attribute__((always_inline)) {
+        static_for<4>([&](auto ic) __attribute__((always_inline)) {
+            constexpr int i = decltype(ic)::value;
+            __builtin_amdgcn_raw_buffer_store_b64(codes(i, general, [&](int e) { return BlockDivisor{get8(y, e), get8(s, e)}; }), r,
+                                                  at, 32 * i * K, kNt);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    if (odd) out(std::true_type{});
+    else out(std::false_type{});
 }
 
-template <typename TX>
-static hipError_t launch_tile(const TileArgs &a, int format, hipStream_t stream) {
+template <typename TX, bool kW>
+static hipError_t launch_tile_w(const TileArgs &a, int format, hipStream_t stream) {
     const int64_t grid = (int64_t)a.tiles_m * (a.K / 128);
     if (!grid_fits(grid, 512)) return hipErrorInvalidValue;
     const dim3 g((unsigned)grid), b(512);
-    if (format == kSfFp32) hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfFp32>), g, b, 0, stream, a);
-    else if (format == kSfUe8m0) hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfUe8m0>), g, b, 0, stream, a);
-    else hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfPacked>), g, b, 0, stream, a);
+    if (format == kSfFp32) hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfFp32, kW>), g, b, 0, stream, a);
+    else if (format == kSfUe8m0) hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfUe8m0, kW>), g, b, 0, stream, a);
+    else hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfPacked, kW>), g, b, 0, stream, a);
     return hipGetLastError();
+}
+
+template <typename TX>
+static hipError_t launch_tile(const MoeDispatchProblem &p, hipStream_t stream) {
+    // mul = ceil(2^(31 + l) / top_k) with 2^(l - 1) < top_k <= 2^l is below 2^32,
+    // and at most top_k - 1 too large times top_k: for pair < 2^31 that moves the
+    // quotient by less than 2^-l, and its fraction is at most 1 - 1 / top_k
+    int l = 0;
+    while (((int64_t)1 << l) < p.top_k) ++l;
+    const uint64_t mul = (((uint64_t)1 << (31 + l)) + p.top_k - 1) / p.top_k;
+    const TileArgs a{p.x, p.weights, p.src, p.y, p.q, p.sf, p.qt, p.sft, p.ld_x, p.T * p.top_k, p.K, p.R, p.R / 128,
+                     (uint32_t)mul, l};
+    return p.weights ? launch_tile_w<TX, true>(a, p.format, stream) : launch_tile_w<TX, false>(a, p.format, stream);
 }
 
 // By tile where column-scaled codes are wanted (every output but dw then comes
@@ -637,8 +803,7 @@ hipError_t launch_moe_dispatch(const MoeDispatchProblem &p, int num_cus, hipStre
         if (err != hipSuccess) return err;
     }
     if (!tile) return hipSuccess;
-    const TileArgs a{p.x, p.weights, p.src, p.y, p.q, p.sf, p.qt, p.sft, p.ld_x, p.T * p.top_k, p.top_k, p.K, p.R, p.R / 128};
-    return p.x_type == kBf16 ? launch_tile<uint16_t>(a, p.format, stream) : launch_tile<float>(a, p.format, stream);
+    return p.x_type == kBf16 ? launch_tile<uint16_t>(p, stream) : launch_tile<float>(p, stream);
 }
 
 // ---------------------------------------------------------------- dispatch of codes

@@ -268,7 +268,8 @@ def test_dispatch_with_weights(xt, scales, T, K):
     check_cols(s, v, qt, sft, scales, "by tile")
 
 
-def test_dispatch_special_values():
+@pytest.mark.parametrize("xt", [BF16, F32])
+def test_dispatch_special_values(xt):
     """NaN, infinities and zeros, in tokens that are dropped and in others, with weights that are such themselves: codes
     and scales as the quantiser's on the fp32 products, by token and by tile."""
     announce("dispatch special values")
@@ -276,7 +277,7 @@ def test_dispatch_special_values():
     ids = random_ids(5, T, k, G, drop=0.2)
     x = normal(5, (T, K))
     x[0, 3], x[1, 130], x[2], x[3, :128], x[4, 5] = np.nan, np.inf, 0.0, np.nan, -np.inf
-    x = device(x)
+    x = device(x, xt)
     w = normal(6, (T, k))
     w[5, 0], w[6, 1], w[1, 0], w[2, 1], w[7] = np.nan, np.inf, 0.0, np.inf, 0.0
     w = device(w)
@@ -295,6 +296,13 @@ def test_dispatch_special_values():
             assert np.array_equal(q.cpu().numpy()[live], want_q[s[live]])
             assert np.array_equal(sf.cpu().numpy().T[live], want_sf[s[live]])
             assert np.all(q.cpu().numpy()[~live] == SENTINEL["q"])
+            if cols:                                   # the columns of each 128 rows, through the same quantiser
+                full = torch.zeros((R, K), device="cuda")
+                full[torch.from_numpy(live).cuda()] = v[torch.from_numpy(s[live]).cuda().long()]
+                _, _, qt, sft, _ = dg.moe_dispatch_quantize_e4m3_contiguous(x, rows, R, src=src, weights=weights, q=False, qt=True)
+                for b in range(R // 128):
+                    cq, csf = dg.quantize_e4m3_1x128(full[128 * b:128 * b + 128].t().contiguous())
+                    assert torch.equal(qt[128 * b:128 * b + 128].t(), cq) and torch.equal(sft[b], csf[0, :K])
 
 
 def test_dispatch_column_codes_alone_and_empty():
