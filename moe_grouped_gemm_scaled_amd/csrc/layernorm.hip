@@ -231,16 +231,31 @@ struct LnBwdArgs {
     float eps;
 };
 
+// Waves of a workgroup and workgroups of a CU: as many rows side by side as
+// registers allow (h, dy and dres of the row, h and dy of the next, sums of dw
+// and db), in one workgroup rather than in two where that costs no time, because
+// each workgroup leaves partial rows of dw and db.  Eight waves: 4096 rows of
+// 7168: 57.3 us, 60.0 with two workgroups of four; 16384 of 1024: 31.0, 31.6;
+// two such workgroups per CU where a thread holds 8 columns: 16384 rows of 2048:
+// 63.0, 76.5 with four waves, 82 with one workgroup; sixteen waves: 60.6 there,
+// but 9.9 against 8.7 for 333 rows.
+template <int WPR, int NCH>
+struct LnBwdShape {
+    static constexpr int kThreads = 512;
+    static constexpr int kRows = kThreads / (64 * WPR);   // side by side
+    static constexpr int kPerCu = WPR == 4 && NCH == 1 ? 2 : 1;
+};
+
 // WPR waves share a row; the workgroup walks its own run of consecutive rows,
-// NR = 4 / WPR of them at a time (WPR < 4), and keeps its sums of dw and db in
-// registers (each lane owns the same columns of every row).  The next row's h
-// and dy are loaded while the current row is reduced.  dw and db leave as one
-// fp32 row each per workgroup, added up in workgroup order by a second kernel:
-// the same bits on every run.
+// NR of them at a time, and keeps its sums of dw and db in registers (each lane
+// owns the same columns of every row).  The next row's h and dy are loaded while
+// the current row is reduced.  dw and db leave as one fp32 row each per
+// workgroup, added up in workgroup order by a second kernel: the same bits on
+// every run.
 template <typename TH, typename TY, typename TW, int WPR, int NCH>
-__global__ void __launch_bounds__(WPR <= 4 ? 256 : 64 * WPR)
+__global__ void __launch_bounds__(512)
 layernorm_bwd_kernel(LnBwdArgs p) {
-    constexpr int NR = WPR < 4 ? 4 / WPR : 1;          // rows at a time
+    constexpr int NR = LnBwdShape<WPR, NCH>::kRows;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int w0 = wave % WPR, r0 = wave / WPR;
@@ -271,9 +286,9 @@ layernorm_bwd_kernel(LnBwdArgs p) {
             yn[c] = load8<true>(Y + row * K + at[c]);
         });
     };
-    // WPR >= 4: sums over the row's waves.  Each array is written again only
+    // WPR > 1: sums over the row's waves.  Each array is written again only
     // behind the other one's barrier, so behind every read of it.
-    __shared__ float2 red1[WPR], red2[WPR];
+    __shared__ float2 red1[NR][WPR], red2[NR][WPR];
     const int64_t n_it = (hi - lo + NR - 1) / NR;
     if (n_it > 0) fetch(lo + r0 < hi ? lo + r0 : hi - 1);
     for (int64_t it = 0; it < n_it; ++it) {
@@ -296,7 +311,7 @@ layernorm_bwd_kernel(LnBwdArgs p) {
         auto over_row = [&](float2 v, float2 *red) __attribute__((always_inline)) {
             v.x = sum64(v.x);
             v.y = sum64(v.y);
-            if constexpr (WPR >= 4) {
+            if constexpr (WPR > 1) {
                 if (lane == 0) red[w0] = v;
                 __syncthreads();
                 v = float2{0.f, 0.f};
@@ -319,7 +334,7 @@ layernorm_bwd_kernel(LnBwdArgs p) {
                 }
             }
         });
-        a = over_row(a, red1);
+        a = over_row(a, red1[r0]);
         const float mean = a.x / (float)K, mg = a.y / (float)K;
         static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
             constexpr int c = decltype(cc)::value;
@@ -332,7 +347,7 @@ layernorm_bwd_kernel(LnBwdArgs p) {
                 }
             }
         });
-        b = over_row(b, red2);
+        b = over_row(b, red2[r0]);
         const float r = 1.0f / sqrtf(b.x / (float)K + p.eps);
         const float k = r * r * (b.y / (float)K);      // n * mean(g n) = d * k
         if (live) {
@@ -351,25 +366,34 @@ layernorm_bwd_kernel(LnBwdArgs p) {
             });
         }
     }
-    // one fp32 row each per workgroup; rows handled side by side (WPR < 4) first
-    // add up through LDS, in wave order
-    auto leave = [&](const float (&v)[NCH][8], float *dst) __attribute__((always_inline)) {
+    // one fp32 row each per workgroup: of the rows handled side by side, the first
+    // one's waves add the others' to theirs, in order (a single row leaves as it is)
+    auto leave = [&](float (&v)[NCH][8], float *dst) __attribute__((always_inline)) {
         float *out = dst + (int64_t)blockIdx.x * p.stride;
         if constexpr (NR > 1) {
-            __shared__ float part[NR][WPR * NCH * 512];
-            static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
-                constexpr int c = decltype(cc)::value;
-                store8(&part[r0][col[c]], v[c]);
-            });
-            __syncthreads();
-            for (int j = threadIdx.x; j < K; j += 256) {
-                float s = part[0][j];
-#pragma unroll
-                for (int q = 1; q < NR; ++q) s += part[q][j];
-                out[j] = s;
+            __shared__ __attribute__((aligned(16))) float part[NR - 1][WPR * NCH * 512];
+            const bool join = hi - lo > 1;             // uniform
+            if (join && r0 > 0) {
+                static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
+                    constexpr int c = decltype(cc)::value;
+                    store8(&part[r0 - 1][col[c]], v[c]);
+                });
             }
-            __syncthreads();
-        } else {
+            if (join) __syncthreads();
+            if (join && r0 == 0) {
+                static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
+                    constexpr int c = decltype(cc)::value;
+#pragma unroll
+                    for (int q = 0; q < NR - 1; ++q) {
+                        const Raw8<float> o = load8(&part[q][col[c]]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[c][i] += get8(o, i);
+                    }
+                });
+            }
+            if (join) __syncthreads();
+        }
+        if (r0 == 0) {
             static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
                 constexpr int c = decltype(cc)::value;
                 if (col[c] < K) store8(out + col[c], v[c]);
@@ -403,18 +427,18 @@ __global__ void __launch_bounds__(1024) layernorm_dw_kernel(const float *__restr
     }
 }
 
-// Workgroups of the backward pass, as in the RMS norm's: one for a few short
-// rows (no second kernel), a row each up to as many rows as CUs, two rows or
-// more above; two workgroups per CU at most, one above 8192 columns.
-static int bwd_groups(int rows, int K, int num_cus) {
-    if ((int64_t)rows * K < 16384) return 1;
-    const int64_t most = K > 8192 ? num_cus : 2 * (int64_t)num_cus;
-    const int64_t g = rows <= num_cus ? rows : ((int64_t)rows + 1) / 2;
-    return (int)(g < most ? (g > 0 ? g : 1) : most);
+// Workgroups of the backward pass, each of which takes `at_once` rows side by
+// side: one where it takes its rows in two steps (no second kernel, whose launch
+// costs more), else as many as the rows fill.  The workspace covers every shape:
+// its groups are counted with one row at a time and two per CU.
+static int bwd_groups(int rows, int at_once, int most) {
+    if (rows <= 2 * at_once) return 1;
+    const int64_t g = ((int64_t)rows + at_once - 1) / at_once;
+    return (int)(g < most ? g : most);
 }
 
 size_t layernorm_bwd_workspace(int rows, int K, int num_cus) {
-    const int g = bwd_groups(rows, K, num_cus);
+    const int g = bwd_groups(rows, 1, 2 * num_cus);
     return g > 1 ? (size_t)g * 2 * K * sizeof(float) : 0;
 }
 
@@ -425,13 +449,15 @@ static hipError_t launch_dw(const float *part, int n, const LayerNormBwdProblem 
 }
 
 template <typename TH, typename TY, typename TW, int WPR, int NCH>
-static hipError_t launch_bwd_t(const LayerNormBwdProblem &p, int groups, hipStream_t stream) {
+static hipError_t launch_bwd_t(const LayerNormBwdProblem &p, int num_cus, hipStream_t stream) {
+    using Shape = LnBwdShape<WPR, NCH>;
+    const int groups = bwd_groups(p.rows, Shape::kRows, Shape::kPerCu * num_cus);
     float *part = static_cast<float *>(p.ws);
     const bool parts = groups > 1;
     const LnBwdArgs a{p.dy, p.h, p.weight, p.dres, p.dx, p.dw && parts ? part : p.dw, p.db && parts ? part + p.K : p.db,
                       2 * (int64_t)p.K, p.rows, p.K, p.eps};
-    hipLaunchKernelGGL((layernorm_bwd_kernel<TH, TY, TW, WPR, NCH>), dim3((unsigned)groups),
-                       dim3(WPR <= 4 ? 256 : 64 * WPR), 0, stream, a);
+    hipLaunchKernelGGL((layernorm_bwd_kernel<TH, TY, TW, WPR, NCH>), dim3((unsigned)groups), dim3(Shape::kThreads), 0, stream,
+                       a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || !parts || (!p.dw && !p.db)) return err;
     return launch_dw(part, groups, p, stream);
@@ -439,14 +465,13 @@ static hipError_t launch_bwd_t(const LayerNormBwdProblem &p, int groups, hipStre
 
 template <typename TH, typename TY, typename TW>
 static hipError_t launch_bwd_k(const LayerNormBwdProblem &p, int num_cus, hipStream_t stream) {
-    const int g = bwd_groups(p.rows, p.K, num_cus);
     const int n = (p.K + 511) / 512;
-    if (n <= 1) return launch_bwd_t<TH, TY, TW, 1, 1>(p, g, stream);
-    if (n <= 2) return launch_bwd_t<TH, TY, TW, 1, 2>(p, g, stream);
-    if (n <= 4) return launch_bwd_t<TH, TY, TW, 4, 1>(p, g, stream);
-    if (n <= 8) return launch_bwd_t<TH, TY, TW, 4, 2>(p, g, stream);
-    if (n <= 16) return launch_bwd_t<TH, TY, TW, 4, 4>(p, g, stream);
-    if (n <= 32) return launch_bwd_t<TH, TY, TW, 8, 4>(p, g, stream);
+    if (n <= 1) return launch_bwd_t<TH, TY, TW, 1, 1>(p, num_cus, stream);
+    if (n <= 2) return launch_bwd_t<TH, TY, TW, 1, 2>(p, num_cus, stream);
+    if (n <= 4) return launch_bwd_t<TH, TY, TW, 4, 1>(p, num_cus, stream);
+    if (n <= 8) return launch_bwd_t<TH, TY, TW, 4, 2>(p, num_cus, stream);
+    if (n <= 16) return launch_bwd_t<TH, TY, TW, 4, 4>(p, num_cus, stream);
+    if (n <= 32) return launch_bwd_t<TH, TY, TW, 8, 4>(p, num_cus, stream);
     return hipErrorInvalidValue;
 }
 
