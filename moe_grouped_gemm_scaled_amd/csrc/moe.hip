@@ -16,6 +16,22 @@
 
 namespace dg {
 
+// Division of numbers below 2^31 by a number known to the host: n / d =
+// (n * mul) >> (31 + l) with mul = ceil(2^(31 + l) / d) and 2^(l - 1) < d <= 2^l.
+// mul is below 2^32, and d * mul at most d - 1 above 2^(31 + l), which moves the
+// quotient of n < 2^31 by less than 1 / d, while its fraction is at most 1 - 1 / d.
+struct Divisor {
+    uint32_t mul = 0;
+    int shift = 0;
+    explicit Divisor(int d) {
+        int l = 0;
+        while (((int64_t)1 << l) < d) ++l;
+        mul = (uint32_t)((((uint64_t)1 << (31 + l)) + (uint32_t)d - 1) / (uint32_t)d);
+        shift = 31 + l;
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return (uint32_t)(((uint64_t)n * mul) >> shift); }
+};
+
 // ---------------------------------------------------------------- sort
 
 struct SortArgs {
@@ -338,33 +354,39 @@ moe_dispatch_kernel(DispatchArgs p) {
     const float *ws = kW ? p.weights + (int64_t)tok * p.top_k : nullptr;
 
     const TX *xr = static_cast<const TX *>(p.x) + (int64_t)tok * p.ld_x;
-    Raw16<TX> xv[NCH];
-    int col[NCH];
-    static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
-        constexpr int c = decltype(cc)::value;
-        col[c] = 16 * (64 * (WPR * c + w0) + lane);
-        xv[c] = load16(xr + min(col[c], K - 16));
-    });
+    // up to 64 choices' rows and weights in the lanes of a wave: one load, not one after the other
+    auto row_of = [&](int j0) __attribute__((always_inline)) { return j0 + lane < j_hi ? rows[j0 + lane] : -1; };
+    auto weight_of = [&](int j0) __attribute__((always_inline)) { return kW && j0 + lane < j_hi ? ws[j0 + lane] : 0.f; };
+    int row64 = row_of(j_lo);
     if constexpr (kDot) {
+        // 8 columns per lane here, so that a load reads 1 KB of a row of ye
+        Raw8<TX> xd[2 * NCH];
+        int cold[2 * NCH];
+        static_for<2 * NCH>([&](auto cc) __attribute__((always_inline)) {
+            constexpr int c = decltype(cc)::value;
+            cold[c] = 8 * (64 * (WPR * c + w0) + lane);
+            xd[c] = load8(xr + min(cold[c], K - 8));
+        });
         __shared__ float red[kBatch][WPR];
         for (int j0 = j_lo; j0 < j_hi; j0 += kBatch) {
+            const int rj = j0 == j_lo ? row64 : row_of(j0);
             static_for<kBatch>([&](auto jc) __attribute__((always_inline)) {
                 constexpr int j = decltype(jc)::value;
                 if (j0 + j < j_hi) {                   // uniform
-                    const int r = rows[j0 + j];
+                    const int r = __builtin_amdgcn_readlane(rj, j);
                     float d = 0.f;
                     if ((unsigned)r < (unsigned)p.R) {
                         const uint16_t *yr = p.ye + (int64_t)r * K;
-                        Raw16<uint16_t> yv[NCH];
-                        static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
+                        Raw8<uint16_t> yv[2 * NCH];
+                        static_for<2 * NCH>([&](auto cc) __attribute__((always_inline)) {
                             constexpr int c = decltype(cc)::value;
-                            yv[c] = load16(yr + min(col[c], K - 16));
+                            yv[c] = load8<true>(yr + min(cold[c], K - 8));
                         });
-                        static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
+                        static_for<2 * NCH>([&](auto cc) __attribute__((always_inline)) {
                             constexpr int c = decltype(cc)::value;
-                            if (col[c] < K) {
+                            if (cold[c] < K) {
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) d = __builtin_fmaf(get16(xv[c], i), get16(yv[c], i), d);
+                                for (int i = 0; i < 8; ++i) d = __builtin_fmaf(get8(xd[c], i), get8(yv[c], i), d);
                             }
                         });
                         d = sum64(d);
@@ -389,6 +411,13 @@ moe_dispatch_kernel(DispatchArgs p) {
         }
     }
     if (!p.q && !p.y) return;                          // uniform
+    Raw16<TX> xv[NCH];
+    int col[NCH];
+    static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
+        constexpr int c = decltype(cc)::value;
+        col[c] = 16 * (64 * (WPR * c + w0) + lane);
+        xv[c] = load16(xr + min(col[c], K - 16));
+    });
     // ---- the blocks' maxima, in registers and LDS
     __shared__ float maxima[WPR == 1 ? 4 : 1][8 * WPR * NCH];
     float *bmax = maxima[WPR == 1 ? wave : 0];
@@ -422,54 +451,59 @@ moe_dispatch_kernel(DispatchArgs p) {
         if constexpr (WPR > 1) __syncthreads();
         else __builtin_amdgcn_wave_barrier();          // one wave's LDS accesses stay in order
     }
-    // ---- the rows
-    for (int j = j_lo; j < j_hi; ++j) {
-        const int r = rows[j];                         // uniform
-        if ((unsigned)r >= (unsigned)p.R) continue;
-        const float w = kW ? ws[j] : 1.f;
-        static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
-            constexpr int c = decltype(cc)::value;
-            if (p.q) {
-                if constexpr (kW) code[c] = encode(c, w, fabsf(w) * amax[c]);
-                if (col[c] < K)
-                    __builtin_nontemporal_store(__builtin_bit_cast(v4i, code[c]),
-                                                reinterpret_cast<v4i *>(p.q + (int64_t)r * K + col[c]));
-            }
-            if (p.y && col[c] < K) {
-                float lo[8], hi[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    lo[i] = kW ? w * get16(xv[c], i) : get16(xv[c], i);
-                    hi[i] = kW ? w * get16(xv[c], i + 8) : get16(xv[c], i + 8);
-                }
-                uint16_t *dst = p.y + (int64_t)r * K + col[c];
-                store8<true>(dst, lo);
-                store8<true>(dst + 8, hi);
-            }
-        });
-    }
-    if (!p.q) return;
-    // ---- their scales, a row per wave at a time
     const int blocks = K / kKBlock, words = p.format == kSfPacked ? (blocks + 3) / 4 : blocks;
-    for (int j = j_lo + w0; j < j_hi; j += WPR) {
-        const int r = rows[j];
-        if ((unsigned)r >= (unsigned)p.R) continue;
-        const float w = kW ? fabsf(ws[j]) : 1.f;
-        const int g = p.cap == p.R ? 0 : r / p.cap;
-        uint32_t *sf = static_cast<uint32_t *>(p.sf) + g * p.sf_group + (r - g * p.cap);
-        for (int b = lane; b < words; b += 64) {
-            uint32_t word;
-            if (p.format == kSfPacked) {
-                word = 0;
+    for (int j0 = j_lo; j0 < j_hi; j0 += 64) {
+        if (j0 > j_lo) row64 = row_of(j0);
+        const float weight64 = weight_of(j0);
+        const int n = min(j_hi - j0, 64);
+        // ---- the rows
+        for (int j = 0; j < n; ++j) {
+            const int r = __builtin_amdgcn_readlane(row64, j);
+            if ((unsigned)r >= (unsigned)p.R) continue;
+            const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight64), j));
+            static_for<NCH>([&](auto cc) __attribute__((always_inline)) {
+                constexpr int c = decltype(cc)::value;
+                if (p.q) {
+                    if constexpr (kW) code[c] = encode(c, w, fabsf(w) * amax[c]);
+                    if (col[c] < K)
+                        __builtin_nontemporal_store(__builtin_bit_cast(v4i, code[c]),
+                                                    reinterpret_cast<v4i *>(p.q + (int64_t)r * K + col[c]));
+                }
+                if (p.y && col[c] < K) {
+                    float lo[8], hi[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (4 * b + i < blocks)
-                        word |= (__float_as_uint(block_scale<true>(kW ? w * bmax[4 * b + i] : bmax[4 * b + i])) >> 23) << (8 * i);
-            } else {
-                const float m = kW ? w * bmax[b] : bmax[b];
-                word = __float_as_uint(p.format == kSfFp32 ? block_scale<false>(m) : block_scale<true>(m));
+                    for (int i = 0; i < 8; ++i) {
+                        lo[i] = kW ? w * get16(xv[c], i) : get16(xv[c], i);
+                        hi[i] = kW ? w * get16(xv[c], i + 8) : get16(xv[c], i + 8);
+                    }
+                    uint16_t *dst = p.y + (int64_t)r * K + col[c];
+                    store8<true>(dst, lo);
+                    store8<true>(dst + 8, hi);
+                }
+            });
+        }
+        if (!p.q) continue;
+        // ---- their scales, a row per wave at a time
+        for (int j = w0; j < n; j += WPR) {
+            const int r = __builtin_amdgcn_readlane(row64, j);
+            if ((unsigned)r >= (unsigned)p.R) continue;
+            const float w = fabsf(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight64), j)));
+            const int g = p.cap == p.R ? 0 : r / p.cap;
+            uint32_t *sf = static_cast<uint32_t *>(p.sf) + g * p.sf_group + (r - g * p.cap);
+            for (int b = lane; b < words; b += 64) {
+                uint32_t word;
+                if (p.format == kSfPacked) {
+                    word = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (4 * b + i < blocks)
+                            word |= (__float_as_uint(block_scale<true>(kW ? w * bmax[4 * b + i] : bmax[4 * b + i])) >> 23) << (8 * i);
+                } else {
+                    const float m = kW ? w * bmax[b] : bmax[b];
+                    word = __float_as_uint(p.format == kSfFp32 ? block_scale<false>(m) : block_scale<true>(m));
+                }
+                sf[(int64_t)b * p.ld_sf] = word;
             }
-            sf[(int64_t)b * p.ld_sf] = word;
         }
     }
 }
@@ -520,8 +554,7 @@ struct TileArgs {
     float *sft;
     int64_t ld_x;
     int pairs, K, R, tiles_m;
-    uint32_t mul;      // pair / top_k = (pair * mul) >> (31 + shift), exactly for pair < 2^31
-    int shift;
+    Divisor by_top_k;
 };
 
 // Magnitudes as integers, whose order is that of the numbers, with infinities
@@ -638,7 +671,7 @@ __global__ void __launch_bounds__(512, 4) moe_dispatch_tile_kernel(TileArgs p) {
             w[i] = 0.f;
             if ((unsigned)pair[i] < (unsigned)p.pairs) {
                 held |= 1u << i;
-                const int64_t tok = (int64_t)(((uint64_t)(uint32_t)pair[i] * p.mul) >> (31 + p.shift));
+                const int64_t tok = p.by_top_k.quotient((uint32_t)pair[i]);
                 raw[i] = load8(static_cast<const TX *>(p.x) + tok * p.ld_x + n0 + c8);
                 if constexpr (kW) w[i] = p.weights[pair[i]];
             }
@@ -779,14 +812,8 @@ static hipError_t launch_tile_w(const TileArgs &a, int format, hipStream_t strea
 
 template <typename TX>
 static hipError_t launch_tile(const MoeDispatchProblem &p, hipStream_t stream) {
-    // mul = ceil(2^(31 + l) / top_k) with 2^(l - 1) < top_k <= 2^l is below 2^32,
-    // and at most top_k - 1 too large times top_k: for pair < 2^31 that moves the
-    // quotient by less than 2^-l, and its fraction is at most 1 - 1 / top_k
-    int l = 0;
-    while (((int64_t)1 << l) < p.top_k) ++l;
-    const uint64_t mul = (((uint64_t)1 << (31 + l)) + p.top_k - 1) / p.top_k;
     const TileArgs a{p.x, p.weights, p.src, p.y, p.q, p.sf, p.qt, p.sft, p.ld_x, p.T * p.top_k, p.K, p.R, p.R / 128,
-                     (uint32_t)mul, l};
+                     Divisor(p.top_k)};
     return p.weights ? launch_tile_w<TX, true>(a, p.format, stream) : launch_tile_w<TX, false>(a, p.format, stream);
 }
 
@@ -821,22 +848,27 @@ struct CopyArgs {
 // A workgroup of 256 threads per token: its codes (16 per lane) and scales are
 // read once and written to each of its rows.
 __global__ void __launch_bounds__(256) moe_dispatch_codes_kernel(CopyArgs p) {
+    const int lane = threadIdx.x & 63;
     const int tok = xcd_remap(blockIdx.x, gridDim.x);
     const int32_t *rows = p.rows + (int64_t)tok * p.top_k;
-    for (int c = threadIdx.x; c < p.K / 16; c += 256) {
-        const v4i v = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(p.x + (int64_t)tok * p.K) + c);
-        for (int j = 0; j < p.top_k; ++j) {
-            const int r = rows[j];
-            if ((unsigned)r < (unsigned)p.R) reinterpret_cast<v4i *>(p.q + (int64_t)r * p.K)[c] = v;
+    for (int j0 = 0; j0 < p.top_k; j0 += 64) {
+        const int n = min(p.top_k - j0, 64);
+        const int row64 = lane < n ? rows[j0 + lane] : -1;   // in the lanes: one load, not one after the other
+        for (int b = threadIdx.x; b < p.words; b += 256) {
+            const uint32_t s = p.sf_in[(int64_t)b * p.ld_in + tok];
+            for (int j = 0; j < n; ++j) {
+                const int r = __builtin_amdgcn_readlane(row64, j);
+                if ((unsigned)r >= (unsigned)p.R) continue;
+                const int g = p.cap == p.R ? 0 : r / p.cap;
+                p.sf[g * p.sf_group + (int64_t)b * p.ld_sf + (r - g * p.cap)] = s;
+            }
         }
-    }
-    for (int b = threadIdx.x; b < p.words; b += 256) {
-        const uint32_t s = p.sf_in[(int64_t)b * p.ld_in + tok];
-        for (int j = 0; j < p.top_k; ++j) {
-            const int r = rows[j];
-            if ((unsigned)r >= (unsigned)p.R) continue;
-            const int g = r / p.cap;
-            p.sf[g * p.sf_group + (int64_t)b * p.ld_sf + (r - g * p.cap)] = s;
+        for (int c = threadIdx.x; c < p.K / 16; c += 256) {
+            const v4i v = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(p.x + (int64_t)tok * p.K) + c);
+            for (int j = 0; j < n; ++j) {
+                const int r = __builtin_amdgcn_readlane(row64, j);
+                if ((unsigned)r < (unsigned)p.R) __builtin_nontemporal_store(v, reinterpret_cast<v4i *>(p.q + (int64_t)r * p.K) + c);
+            }
         }
     }
 }
@@ -857,49 +889,53 @@ struct CombineArgs {
     const void *res;
     void *out;
     int T, top_k, K, R, chunks;   // 512-column chunks of a row
+    Divisor by_chunks;
 };
 
 // A wave per token and 512 columns (lane l: columns 8 l .. 8 l + 7 of them);
-// nothing is shared between waves, and the loads of eight choices are in flight
-// together.  The sum runs in the order of the choices, in fp32.
-template <typename TO, bool kRes, bool kW>
+// nothing is shared between waves.  kBatch choices at a time, whose loads are all
+// in flight together: a choice without a row reads row 0 (and counts as nothing),
+// since a load under a condition waits for the one before it (64 tokens of 7168,
+// 8 choices: 4.3 us, 6.9 so).  Four of them: 4096 tokens 103.6 us in a graph, 4.6
+// TB/s of rows; all 8 at once, 103.5, and 4.6 for the 64.  Workgroups in launch
+// order: 112 us with neighbours on one XCD.  The sum runs in the order of the
+// choices, in fp32.
+template <typename TO, bool kRes, bool kW, int kBatch>
 __global__ void __launch_bounds__(256) moe_combine_kernel(CombineArgs p) {
-    constexpr int kBatch = 8;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t item = (int64_t)xcd_remap(blockIdx.x, gridDim.x) * 4 + wave;
-    const int64_t tok = item / p.chunks;
+    const uint32_t item = blockIdx.x * 4 + wave;     // below 2^26
+    const int tok = (int)p.by_chunks.quotient(item);
     if (tok >= p.T) return;
     const int K = p.K, top_k = p.top_k;
-    const int col = (int)(item - tok * p.chunks) * 512 + 8 * lane;
+    const int col = (int)(item - (uint32_t)tok * p.chunks) * 512 + 8 * lane;
     const bool in = col < K;
     const int at = min(col, K - 8);
-    const int32_t *rows = p.rows + tok * top_k;
+    const int32_t *rows = p.rows + (int64_t)tok * top_k;
+    const float *ws = kW ? p.weights + (int64_t)tok * top_k : nullptr;
+    Raw8<TO> res{};
+    if constexpr (kRes) res = load8<true>(static_cast<const TO *>(p.res) + (int64_t)tok * K + at);
     float acc[8];
-    if constexpr (kRes) {
-        const Raw8<TO> r = load8<true>(static_cast<const TO *>(p.res) + tok * K + at);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = get8(r, i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    }
     for (int j0 = 0; j0 < top_k; j0 += kBatch) {
         Raw8<uint16_t> v[kBatch];
         bool live[kBatch];
         float w[kBatch];
+        int r[kBatch];
+        // past the last choice, that one's entry again
         static_for<kBatch>([&](auto jc) __attribute__((always_inline)) {
             constexpr int j = decltype(jc)::value;
-            live[j] = false;
-            if (j0 + j < top_k) {                      // uniform
-                const int r = rows[j0 + j];
-                live[j] = (unsigned)r < (unsigned)p.R;
-                if (live[j]) {
-                    v[j] = load8<true>(p.y + (int64_t)r * K + at);
-                    if constexpr (kW) w[j] = p.weights[tok * top_k + j0 + j];
-                }
-            }
+            r[j] = rows[min(j0 + j, top_k - 1)];
+            w[j] = kW ? ws[min(j0 + j, top_k - 1)] : 1.f;
         });
+        static_for<kBatch>([&](auto jc) __attribute__((always_inline)) {
+            constexpr int j = decltype(jc)::value;
+            live[j] = j0 + j < top_k && (unsigned)r[j] < (unsigned)p.R;     // uniform
+            v[j] = load8<true>(p.y + (int64_t)(live[j] ? r[j] : 0) * K + at);
+        });
+        if (j0 == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = kRes ? get8(res, i) : 0.f;
+        }
         static_for<kBatch>([&](auto jc) __attribute__((always_inline)) {
             constexpr int j = decltype(jc)::value;
             if (live[j]) {
@@ -909,26 +945,52 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(CombineArgs p) {
             }
         });
     }
-    if (in) store8<true>(static_cast<TO *>(p.out) + tok * K + col, acc);
+    if (in) store8<true>(static_cast<TO *>(p.out) + (int64_t)tok * K + col, acc);
+}
+
+template <typename TO, bool kRes, bool kW>
+static hipError_t launch_combine_b(const CombineArgs &a, hipStream_t stream) {
+    const int64_t groups = ((int64_t)a.T * a.chunks + 3) / 4;
+    if (!grid_fits(groups, 256)) return hipErrorInvalidValue;
+    const dim3 g((unsigned)groups), b(256);
+    if (a.top_k <= 2) hipLaunchKernelGGL((moe_combine_kernel<TO, kRes, kW, 2>), g, b, 0, stream, a);
+    else hipLaunchKernelGGL((moe_combine_kernel<TO, kRes, kW, 4>), g, b, 0, stream, a);
+    return hipGetLastError();
 }
 
 template <typename TO>
 static hipError_t launch_combine_t(const CombineArgs &a, hipStream_t stream) {
-    const int64_t groups = ((int64_t)a.T * a.chunks + 3) / 4;
-    if (!grid_fits(groups, 256)) return hipErrorInvalidValue;
-    const dim3 g((unsigned)groups), b(256);
-    if (a.res) {
-        if (a.weights) hipLaunchKernelGGL((moe_combine_kernel<TO, true, true>), g, b, 0, stream, a);
-        else hipLaunchKernelGGL((moe_combine_kernel<TO, true, false>), g, b, 0, stream, a);
-    } else {
-        if (a.weights) hipLaunchKernelGGL((moe_combine_kernel<TO, false, true>), g, b, 0, stream, a);
-        else hipLaunchKernelGGL((moe_combine_kernel<TO, false, false>), g, b, 0, stream, a);
+    if (a.res) return a.weights ? launch_combine_b<TO, true, true>(a, stream) : launch_combine_b<TO, true, false>(a, stream);
+    return a.weights ? launch_combine_b<TO, false, true>(a, stream) : launch_combine_b<TO, false, false>(a, stream);
+}
+
+// Without rows there is nothing to read, not even row 0: out is the residual, or
+// zeros.
+template <typename TO>
+__global__ void __launch_bounds__(256) moe_residual_kernel(const TO *res, TO *out, int64_t n8) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += (int64_t)gridDim.x * 256) {
+        float v[8];
+        const Raw8<TO> r = res ? load8(res + 8 * i) : Raw8<TO>{};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = res ? get8(r, e) : 0.f;
+        store8(out + 8 * i, v);
     }
-    return hipGetLastError();
 }
 
 hipError_t launch_moe_combine(const MoeCombineProblem &p, hipStream_t stream) {
-    const CombineArgs a{p.y, p.weights, p.rows, p.residual, p.out, p.T, p.top_k, p.K, p.R, (p.K + 511) / 512};
+    if (p.R == 0) {
+        const int64_t n8 = (int64_t)p.T * p.K / 8;
+        const dim3 g((unsigned)(n8 < 1 << 18 ? (n8 + 255) / 256 : 1024)), b(256);
+        if (p.out_type == kBf16)
+            hipLaunchKernelGGL(moe_residual_kernel<uint16_t>, g, b, 0, stream, static_cast<const uint16_t *>(p.residual),
+                               static_cast<uint16_t *>(p.out), n8);
+        else
+            hipLaunchKernelGGL(moe_residual_kernel<float>, g, b, 0, stream, static_cast<const float *>(p.residual),
+                               static_cast<float *>(p.out), n8);
+        return hipGetLastError();
+    }
+    const int chunks = (p.K + 511) / 512;
+    const CombineArgs a{p.y, p.weights, p.rows, p.residual, p.out, p.T, p.top_k, p.K, p.R, chunks, Divisor(chunks)};
     return p.out_type == kBf16 ? launch_combine_t<uint16_t>(a, stream) : launch_combine_t<float>(a, stream);
 }
 
