@@ -746,7 +746,9 @@ __global__ void __launch_bounds__(512, 4) moe_dispatch_tile_kernel(TileArgs p) {
             constexpr int i = decltype(ic)::value;
             const v4i o = v4i{(int)pack_bf16x2_rne(value(i, 0), value(i, 1)), (int)pack_bf16x2_rne(value(i, 2), value(i, 3)),
                               (int)pack_bf16x2_rne(value(i, 4), value(i, 5)), (int)pack_bf16x2_rne(value(i, 6), value(i, 7))};
-            __builtin_amdgcn_raw_buffer_store_b128(o, r, held & (1u << i) ? 2 * at : kPast, 64 * i * K, kNt);
+            // the offset in the vector register alone: with a scalar one beside it, gfx950 still reads the data of a
+            // 16-byte store when the next instruction writes them over, and the compiler puts no wait between
+            __builtin_amdgcn_raw_buffer_store_b128(o, r, held & (1u << i) ? 2 * at + 64 * i * K : kPast, 0, kNt);
         });
     }
     if (p.q) {                                         // uniform
