@@ -326,6 +326,22 @@ __device__ __forceinline__ float max_of_8_lanes(float x) {
     return fmaxf(x, moved(std::integral_constant<int, 0x141>{})); // row_half_mirror
 }
 
+// A dot product over K columns is the sum, in order, of those over each run of
+// 512 columns, 8 to a lane: the same bits whichever kernel computes it.
+constexpr int kDotBatch = 4, kDotRuns = kNormMaxK / 512;
+template <typename TX>
+__device__ __forceinline__ float dot_of_run(const Raw8<TX> &x, const Raw8<uint16_t> &y, bool in) {
+    float d = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d = __builtin_fmaf(get8(x, i), get8(y, i), d);
+    return sum64(in ? d : 0.f);
+}
+__device__ __forceinline__ float sum_of_runs(const float *d, int runs) {
+    float s = d[0];
+    for (int c = 1; c < runs; ++c) s += d[c];
+    return s;
+}
+
 // A token's row is read once, quantised (once without weights) and written to
 // each of its rows.  WPR waves share a token (WPR = 1: four tokens per
 // workgroup); lane l of wave w holds the 16 columns from
@@ -341,7 +357,6 @@ __device__ __forceinline__ float max_of_8_lanes(float x) {
 template <typename TX, int WPR, int NCH, bool kW, bool kDot>
 __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR)
 moe_dispatch_kernel(DispatchArgs p) {
-    constexpr int kBatch = 8;                          // choices between two barriers of the dot products
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int blk = xcd_remap(blockIdx.x, gridDim.x);
@@ -367,14 +382,14 @@ moe_dispatch_kernel(DispatchArgs p) {
             cold[c] = 8 * (64 * (WPR * c + w0) + lane);
             xd[c] = load8(xr + min(cold[c], K - 8));
         });
-        __shared__ float red[kBatch][WPR];
-        for (int j0 = j_lo; j0 < j_hi; j0 += kBatch) {
+        __shared__ float runs_of[WPR == 1 ? 4 : 1][kDotBatch][2 * WPR * NCH];
+        float(&red)[kDotBatch][2 * WPR * NCH] = runs_of[WPR == 1 ? wave : 0];
+        for (int j0 = j_lo; j0 < j_hi; j0 += kDotBatch) {
             const int rj = j0 == j_lo ? row64 : row_of(j0);
-            static_for<kBatch>([&](auto jc) __attribute__((always_inline)) {
+            static_for<kDotBatch>([&](auto jc) __attribute__((always_inline)) {
                 constexpr int j = decltype(jc)::value;
                 if (j0 + j < j_hi) {                   // uniform
                     const int r = __builtin_amdgcn_readlane(rj, j);
-                    float d = 0.f;
                     if ((unsigned)r < (unsigned)p.R) {
                         const uint16_t *yr = p.ye + (int64_t)r * K;
                         Raw8<uint16_t> yv[2 * NCH];
@@ -384,30 +399,21 @@ moe_dispatch_kernel(DispatchArgs p) {
                         });
                         static_for<2 * NCH>([&](auto cc) __attribute__((always_inline)) {
                             constexpr int c = decltype(cc)::value;
-                            if (cold[c] < K) {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) d = __builtin_fmaf(get8(xd[c], i), get8(yv[c], i), d);
-                            }
+                            const float s = dot_of_run(xd[c], yv[c], cold[c] < K);
+                            if (lane == 0) red[j][WPR * c + w0] = s;
                         });
-                        d = sum64(d);
-                    }
-                    if constexpr (WPR == 1) {
-                        if (lane == 0) p.dw[(int64_t)tok * p.top_k + j0 + j] = d;
-                    } else {
-                        if (lane == 0) red[j][w0] = d;
                     }
                 }
             });
-            if constexpr (WPR > 1) {
-                __syncthreads();
-                if (threadIdx.x < kBatch && j0 + (int)threadIdx.x < j_hi) {
-                    float d = 0.f;
-#pragma unroll
-                    for (int i = 0; i < WPR; ++i) d += red[threadIdx.x][i];
-                    p.dw[(int64_t)tok * p.top_k + j0 + threadIdx.x] = d;
-                }
-                __syncthreads();
+            if constexpr (WPR > 1) __syncthreads();
+            else __builtin_amdgcn_wave_barrier();      // one wave's LDS accesses stay in order
+            const int j = WPR > 1 ? (int)threadIdx.x : lane;
+            if (j < kDotBatch && j0 + j < j_hi) {
+                const bool held = (unsigned)rows[j0 + j] < (unsigned)p.R;
+                p.dw[(int64_t)tok * p.top_k + j0 + j] = held ? sum_of_runs(red[j], (K + 511) / 512) : 0.f;
             }
+            if constexpr (WPR > 1) __syncthreads();
+            else __builtin_amdgcn_wave_barrier();
         }
     }
     if (!p.q && !p.y) return;                          // uniform
@@ -555,6 +561,11 @@ struct TileArgs {
     int64_t ld_x;
     int pairs, K, R, tiles_m;
     Divisor by_top_k;
+    // kDot: the first T workgroups' work
+    const int32_t *rows;
+    const uint16_t *ye;
+    float *dw;
+    int T, top_k;
 };
 
 // Magnitudes as integers, whose order is that of the numbers, with infinities
@@ -621,6 +632,43 @@ __device__ __forceinline__ uint32_t e4m3_encode4_numbers(float a, float b, float
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
 
+// dw[tok, j] = x[tok] . ye[rows[tok, j]] by a workgroup of 8 waves, each of which
+// takes every 8th run of 512 columns; 4 choices at a time, whose loads are in
+// flight together.  A choice without a row reads row 0 and counts as nothing.
+// `red`: kDotBatch * kDotRuns floats of LDS.
+template <typename TX>
+__device__ __forceinline__ void dot_of_token(const TileArgs &p, int tok, float *red) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t *rows = p.rows + (int64_t)tok * p.top_k;
+    const TX *x = static_cast<const TX *>(p.x) + (int64_t)tok * p.ld_x;
+    const int runs = (p.K + 511) / 512;
+    for (int j0 = 0; j0 < p.top_k; j0 += kDotBatch) {
+        const int mine = lane < kDotBatch && j0 + lane < p.top_k ? rows[j0 + lane] : -1;
+        for (int c = wave; c < runs; c += 8) {
+            const int col = 512 * c + 8 * lane, at = min(col, p.K - 8);
+            const Raw8<TX> xv = load8(x + at);
+            Raw8<uint16_t> yv[kDotBatch];
+            static_for<kDotBatch>([&](auto jc) __attribute__((always_inline)) {
+                constexpr int j = decltype(jc)::value;
+                const int r = __builtin_amdgcn_readlane(mine, j);
+                yv[j] = load8<true>(p.ye + (int64_t)((unsigned)r < (unsigned)p.R ? r : 0) * p.K + at);
+            });
+            static_for<kDotBatch>([&](auto jc) __attribute__((always_inline)) {
+                constexpr int j = decltype(jc)::value;
+                const float s = dot_of_run(xv, yv[j], col < p.K);
+                if (lane == 0) red[kDotRuns * j + c] = s;
+            });
+        }
+        __syncthreads();
+        const int j = threadIdx.x;
+        if (j < kDotBatch && j0 + j < p.top_k) {
+            const bool held = (unsigned)rows[j0 + j] < (unsigned)p.R;
+            p.dw[(int64_t)tok * p.top_k + j0 + j] = held ? sum_of_runs(red + kDotRuns * j, runs) : 0.f;
+        }
+        __syncthreads();
+    }
+}
+
 // Both scale directions of a 128 x 128 tile of the experts' rows at once: 512
 // threads, thread t holds columns 8 (t % 16) .. +7 of rows t / 16 + 32 i
 // (i < 4), so 16 lanes hold a row's 128 columns (its scale is a reduction
@@ -643,16 +691,21 @@ __device__ __forceinline__ uint32_t e4m3_encode4_numbers(float a, float b, float
 // CU (64 registers at most for bf16).  166 us, with weights 165; 192 and 203 with
 // the general arithmetic and addresses throughout; a fixed grid that fetches the
 // next tile ahead needs 80 to 97 registers and takes 190.
-template <typename TX, int FMT, bool kW>
+template <typename TX, int FMT, bool kW, bool kDot>
 __global__ void __launch_bounds__(512, 4) moe_dispatch_tile_kernel(TileArgs p) {
     constexpr bool UE = FMT != kSfFp32;
     constexpr uint32_t kInf = 0x7f800000u;
+    __shared__ __attribute__((aligned(16))) float wmax[32][128];
+    const int tokens = kDot ? p.T : 0;
+    if (kDot && (int)blockIdx.x < tokens) {
+        dot_of_token<TX>(p, blockIdx.x, wmax[0]);
+        return;
+    }
     const int t = threadIdx.x;
     const int c8 = 8 * (t & 15), rg = t >> 4;
-    const int tile = xcd_remap(blockIdx.x, gridDim.x);
+    const int tile = xcd_remap((int)blockIdx.x - tokens, (int)gridDim.x - tokens);
     const int tn = tile / p.tiles_m, tm = tile - tn * p.tiles_m;
     const int K = p.K, n0 = tn * 128, m0 = tm * 128;
-    __shared__ __attribute__((aligned(16))) float wmax[32][128];
     __shared__ __attribute__((aligned(16))) float div_y[128], div_s[128];
     __shared__ int odd;                                // a wave has seen an infinity or NaN
     if (t == 0) odd = 0;
@@ -801,38 +854,33 @@ __global__ void __launch_bounds__(512, 4) moe_dispatch_tile_kernel(TileArgs p) {
     else out(std::false_type{});
 }
 
-template <typename TX, bool kW>
-static hipError_t launch_tile_w(const TileArgs &a, int format, hipStream_t stream) {
-    const int64_t grid = (int64_t)a.tiles_m * (a.K / 128);
+template <typename TX, bool kW, bool kDot>
+static hipError_t launch_tile_f(const TileArgs &a, int format, hipStream_t stream) {
+    const int64_t grid = (int64_t)a.tiles_m * (a.K / 128) + (kDot ? a.T : 0);
     if (!grid_fits(grid, 512)) return hipErrorInvalidValue;
     const dim3 g((unsigned)grid), b(512);
-    if (format == kSfFp32) hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfFp32, kW>), g, b, 0, stream, a);
-    else if (format == kSfUe8m0) hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfUe8m0, kW>), g, b, 0, stream, a);
-    else hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfPacked, kW>), g, b, 0, stream, a);
+    if (format == kSfFp32) hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfFp32, kW, kDot>), g, b, 0, stream, a);
+    else if (format == kSfUe8m0) hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfUe8m0, kW, kDot>), g, b, 0, stream, a);
+    else hipLaunchKernelGGL((moe_dispatch_tile_kernel<TX, kSfPacked, kW, kDot>), g, b, 0, stream, a);
     return hipGetLastError();
 }
 
 template <typename TX>
 static hipError_t launch_tile(const MoeDispatchProblem &p, hipStream_t stream) {
     const TileArgs a{p.x, p.weights, p.src, p.y, p.q, p.sf, p.qt, p.sft, p.ld_x, p.T * p.top_k, p.K, p.R, p.R / 128,
-                     Divisor(p.top_k)};
-    return p.weights ? launch_tile_w<TX, true>(a, p.format, stream) : launch_tile_w<TX, false>(a, p.format, stream);
+                     Divisor(p.top_k), p.rows, p.ye, p.dw, p.T, p.top_k};
+    if (p.dw)
+        return p.weights ? launch_tile_f<TX, true, true>(a, p.format, stream) : launch_tile_f<TX, false, true>(a, p.format, stream);
+    return p.weights ? launch_tile_f<TX, true, false>(a, p.format, stream) : launch_tile_f<TX, false, false>(a, p.format, stream);
 }
 
-// By tile where column-scaled codes are wanted (every output but dw then comes
-// from there), by token otherwise.
+// By tile where column-scaled codes are wanted, by token otherwise.
 hipError_t launch_moe_dispatch(const MoeDispatchProblem &p, int num_cus, hipStream_t stream) {
-    const bool tile = p.qt != nullptr && p.R > 0;
-    const bool token = p.T > 0 && (p.dw || (!tile && (p.q || p.y)));
-    if (token) {
-        const DispatchArgs a{p.x, p.weights, p.rows, p.ye, p.dw, tile ? nullptr : p.y, tile ? nullptr : p.q, p.sf, p.ld_x,
-                             p.sf_group, p.T, p.top_k, p.K, p.R, p.cap, p.ld_sf, p.format};
-        const hipError_t err = p.x_type == kBf16 ? launch_dispatch_w<uint16_t>(a, num_cus, stream)
-                                                 : launch_dispatch_w<float>(a, num_cus, stream);
-        if (err != hipSuccess) return err;
-    }
-    if (!tile) return hipSuccess;
-    return p.x_type == kBf16 ? launch_tile<uint16_t>(p, stream) : launch_tile<float>(p, stream);
+    if (p.qt && p.R > 0) return p.x_type == kBf16 ? launch_tile<uint16_t>(p, stream) : launch_tile<float>(p, stream);
+    if (p.T == 0 || (!p.dw && !p.q && !p.y)) return hipSuccess;
+    const DispatchArgs a{p.x, p.weights, p.rows, p.ye, p.dw, p.y, p.q, p.sf, p.ld_x, p.sf_group, p.T, p.top_k, p.K, p.R, p.cap,
+                         p.ld_sf, p.format};
+    return p.x_type == kBf16 ? launch_dispatch_w<uint16_t>(a, num_cus, stream) : launch_dispatch_w<float>(a, num_cus, stream);
 }
 
 // ---------------------------------------------------------------- dispatch of codes
