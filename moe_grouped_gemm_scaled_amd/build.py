@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libdg.so")
 ARGS = os.path.join(HERE, "_args.so")     # the binding's argument checks, a Python extension module
 SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "decode.hip", "pipelined.hip", "persistent.hip", "mqa.hip", "noalloc.hip", "stream.hip",
            "layer_api.cpp", "norm.hip", "gated.hip", "gated_small.hip", "gated_bwd.hip",
-           "layernorm.hip", "moe.hip"]
+           "moe_api.cpp", "layernorm.hip", "moe.hip"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: no v_pk_{add,mul,fma}_f32 from the compiler.
