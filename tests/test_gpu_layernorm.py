@@ -311,6 +311,22 @@ def test_backward_optional_outputs(rows, K):
     assert torch.equal(dg.layernorm_backward(dy, h, w, EPS, dw=False, db=False, workspace=None)[0], want[0])
 
 
+@pytest.mark.parametrize("cus", [1, 3])
+@pytest.mark.parametrize("rows,K", [(50, 512), (41, 1032), (37, 2048), (30, 4096), (23, 7168), (9, 16384)])
+def test_backward_many_rows_per_workgroup(rows, K, cus):
+    """A workgroup's run of rows: even and odd numbers of them, more than it takes side by side."""
+    announce(f"ln_bwd rows={rows} K={K} on {cus} CUs")
+    dy, h = device(normal(20, (rows, K)), BF16), device(2 * normal(21, (rows, K)) + 1, F32)
+    w = device(1 + 0.3 * normal(22, (K,)), BF16)
+    try:
+        dg.set_num_cus(cus)
+        out = dg.layernorm_backward(dy, h, w, EPS)
+        torch.cuda.synchronize()
+    finally:
+        dg.set_num_cus(0)
+    check_backward(dy, h, w, None, *out, "few CUs")
+
+
 @pytest.mark.parametrize("over", ["dres", "h"])
 def test_backward_in_place(over):
     announce(f"ln_bwd in place over {over}")

@@ -513,6 +513,76 @@ def test_dispatch_gradient_is_combine():
         assert abs(left.sum() - right.sum()) <= 2.0 ** -8 * np.abs(left).sum() + 2.0 ** -20 * np.abs(right).sum()
 
 
+# ---------------------------------------------------------------- many choices, few CUs, limits
+
+def test_more_choices_than_lanes():
+    """A token with more choices than a wave has lanes, and than a batch of loads holds, in every operator."""
+    announce("70 choices")
+    T, k, G, K = 5, 70, 100, 384
+    ids = random_ids(4, T, k, G)
+    rows, src = sort(ids, G)
+    same(rows, plan(ids, G, src.numel())[0], "rows")
+    s, R = src.cpu().numpy(), src.numel()
+    x, w = device(normal(1, (T, K)), BF16), device(normal(2, (T, k)))
+    for weights in (None, w):
+        v = pair_values(x, weights, k)
+        q, sf, y = buffers((), R, K, "fp32")
+        dg.moe_dispatch_quantize_e4m3_contiguous(x, rows, R, weights=weights, q=q, sf=sf, y=y)
+        check_rows(s, v, q, sf, y, "fp32", 0, "by token")
+    q_in, sf_in = dg.quantize_e4m3_1x128(x.float())
+    q, sf, _ = buffers((), R, K, "fp32", y=False)
+    dg.moe_dispatch_e4m3_contiguous(q_in, sf_in, rows, R, q=q, sf=sf)
+    check_rows(s, pair_values(x, None, k), q, sf, None, "fp32", 0, "codes")
+    ye = device(normal(3, (R, K)), BF16)
+    ref, size = combined(ye, rows, w, x)
+    check_bf16(dg.moe_combine(ye, rows, weights=w, residual=x), ref, (k + 2) * U * size, "combine")
+    for cols in (None, True):
+        dw, _, _, _, qt, sft = dg.moe_combine_backward_quantize_e4m3_contiguous(x, ye, rows, w, src=src, dw=True, q=False,
+                                                                                qt=cols)
+        r = rows.cpu().numpy()
+        term = f64(x)[:, None, :] * f64(ye)[np.maximum(r, 0)] * (r >= 0)[:, :, None]
+        check(f64(dw), term.sum(2), SLACK * np.abs(term).sum(2), "dw")
+        if cols:
+            check_cols(s, pair_values(x, w, k), qt, sft, "fp32", "columns")
+
+
+@pytest.mark.parametrize("cus", [1, 5])
+def test_few_compute_units(cus):
+    """The number of workgroups that a token's choices are dealt to changes no result."""
+    announce(f"{cus} CUs")
+    T, k, G, K = 9, 8, 12, 2304
+    ids = random_ids(6, T, k, G)
+    rows, src = sort(ids, G)
+    x, w, R = device(normal(1, (T, K)), BF16), device(normal(2, (T, k))), src.numel()
+    ye = device(normal(3, (R, K)), BF16)
+    want = dg.moe_combine_backward_quantize_e4m3_contiguous(x, ye, rows, w, dw=True, q=True, dy=True)
+    try:
+        dg.set_num_cus(cus)
+        got = dg.moe_combine_backward_quantize_e4m3_contiguous(x, ye, rows, w, dw=True, q=True, dy=True)
+        torch.cuda.synchronize()
+    finally:
+        dg.set_num_cus(0)
+    for a, b in zip(got, want):
+        assert a is b is None or torch.equal(a, b)
+
+
+def test_grid_limit():
+    """A grid that would reach 2^32 threads is refused; the one below it runs."""
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GiB of device memory")
+    announce("grid limit")
+    T = 1 << 26
+    y = torch.arange(1, 129, device="cuda").to(BF16).repeat_interleave(8).view(128, 8)
+    rows = torch.zeros((T, 1), dtype=I32, device="cuda")
+    rows[-5:, 0] = torch.arange(5, dtype=I32, device="cuda")
+    with pytest.raises(dg.DGError, match="HIP"):
+        dg.moe_combine(y, rows)
+    out = dg.moe_combine(y, rows[4:])
+    torch.cuda.synchronize()
+    assert torch.equal(out[-5:], y[:5]) and bool((out[:-5] == 1).all())
+    assert dg.moe_combine(y[:0], rows, out=torch.full((T, 8), 3.0, dtype=BF16, device="cuda")).count_nonzero() == 0
+
+
 # ---------------------------------------------------------------- streams, graphs, sizes
 
 def run_all(ids, x, w, G, bufs):
