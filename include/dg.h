@@ -622,7 +622,9 @@ int dg_gated_backward_quantize_e4m3_ue8m0(const uint16_t *gu, const uint16_t *dh
  *   K                  a multiple of 128 where q is asked for, of 8 otherwise;
  *                      8 to 16384
  * The mean is subtracted before the squares are summed, so a mean that is large
- * beside the spread costs no more bits than h itself holds.
+ * beside the spread costs no more bits than h itself holds.  Sums of squares
+ * overflow fp32 for differences above about 1e19: v is then infinite and y the
+ * bias.  A row with an infinity or NaN in it is NaN throughout (codes 0x7f).
  * Errors as there.
  */
 int dg_layernorm_quantize_e4m3_1x128(const void *x, int x_type, int64_t ld_x,
@@ -653,7 +655,8 @@ int dg_layernorm_quantize_e4m3_1x128_ue8m0_packed(const void *x, int x_type, int
  * weight, dres optional; the rest as for dg_rmsnorm_backward, K a multiple of 8.
  *   workspace: dg_get_layernorm_backward_workspace_size(rows, K) bytes of
  *   device memory, 16-byte aligned (NULL when that is 0, or neither dw nor db
- *   is asked for), of any content.
+ *   is asked for), of any content; calls that may run at the same time (other
+ *   streams, graphs replayed concurrently) need one each.
  */
 int dg_layernorm_backward(const void *dy, int dy_type, const void *h, int h_type,
                           const void *weight, int weight_type, float eps,
@@ -691,7 +694,8 @@ int64_t dg_get_layernorm_backward_workspace_size(int rows, int K);
  *   src      [G][M_cap]   optional
  *   workspace: dg_get_moe_sort_workspace_size(T, top_k, G) bytes of device
  *   memory, 16-byte aligned, of any content; with NULL or too few bytes the
- *   same results take longer where that is not 0.
+ *   same results take longer where that is not 0.  Calls that may run at the
+ *   same time need one each.
  * A call with T = 0 writes the plan of no pairs.
  * Errors: DG_ERR_NULL (ids, rows with T > 0; masked_m); DG_ERR_SHAPE (T < 0,
  * top_k < 1, T * top_k > 2^26, G < 1 or > 1024, M_total < 0 or % 128, M_cap < 1;

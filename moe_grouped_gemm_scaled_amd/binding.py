@@ -811,6 +811,7 @@ def layernorm_quantize_e4m3_1x128(x, weight=None, bias=None, eps=1e-5, residual=
         raise ValueError("x: must have two dimensions, [rows, K]")
     shape = x.shape
     rows, K = shape
+    _int32(rows, "rows")
     pitch, column = x.stride()
     if column != 1 and K > 1:
         raise ValueError("x: columns must be dense")
@@ -870,6 +871,7 @@ def layernorm_backward(dy, h, weight=None, eps=1e-5, dres=None, dx=None, dw=None
     if len(shape) != 2:
         raise ValueError(f"h: shape {tuple(shape)}, expected [rows, K]")
     rows, K = shape
+    _int32(rows, "rows")
     if isinstance(workspace, str) and workspace != "auto":
         raise ValueError(f"workspace {workspace!r}")
     index = _device(h, "h")
@@ -908,6 +910,13 @@ def get_moe_sort_workspace_size(T: int, top_k: int, G: int) -> int:
     return int(v)
 
 
+def _int32(n, name):
+    """A size as the C call takes it: ctypes would drop the high bits of a larger one."""
+    if n > 0x7FFFFFFF:
+        raise ValueError(f"{name}: {n} does not fit 32 bits")
+    return n
+
+
 def _sort_workspace(workspace, T, top_k, G, device):
     if not isinstance(workspace, str):
         return workspace
@@ -927,6 +936,7 @@ def moe_sort_contiguous(ids, G, M_total=None, rows=None, src=None, m_indices=Non
     if ids.dim() != 2:
         raise ValueError("ids[T, top_k]")
     T, top_k = ids.shape
+    _int32(T, "T"), _int32(top_k, "top_k")
     index = _device(ids, "ids")
     if M_total is None:
         M_total = get_moe_rows(T, top_k, G)
@@ -950,6 +960,7 @@ def moe_sort_masked(ids, G, M_cap, rows=None, src=None, masked_m=None, workspace
     if ids.dim() != 2:
         raise ValueError("ids[T, top_k]")
     T, top_k = ids.shape
+    _int32(T, "T"), _int32(top_k, "top_k")
     index = _device(ids, "ids")
     i32, dev = torch.int32, ids.device
     if rows is None or masked_m is None or src is True:
@@ -976,6 +987,7 @@ def _dispatch(name, x, rows, lead, per, src, weights, y, q, sf, qt, sft, scales,
     if x.dim() != 2 or rows.dim() != 2:
         raise ValueError(f"{name}[T, K], rows[T, top_k]")
     T, K = x.shape
+    _int32(T, "T"), _int32(rows.shape[1], "top_k"), _int32(per, "rows")
     pitch, column = x.stride()
     if column != 1 and K > 1:
         raise ValueError(f"{name}: columns must be dense")
@@ -1032,6 +1044,7 @@ def _dispatch_codes(q_in, sf_in, rows, lead, per, q, sf):
     if q_in.dim() != 2 or rows.dim() != 2 or sf_in.dim() != 2:
         raise ValueError("q_in[T, K], sf_in[K/128, ld], rows[T, top_k]")
     T, K = q_in.shape
+    _int32(T, "T"), _int32(rows.shape[1], "top_k"), _int32(per, "rows"), _int32(sf_in.shape[1], "ld")
     index = _device(q_in, "q_in")
     packed = sf_in.dtype is torch.int32
     n, bits, ld = _sf_rows(packed, K // 128), _I32 if packed else _F32, (per + 3) // 4 * 4
@@ -1069,6 +1082,8 @@ def moe_combine(y, rows, weights=None, residual=None, out=None):
         raise ValueError("y[.., K], rows[T, top_k]")
     pairs = rows.shape
     T, K = pairs[0], y.shape[-1]
+    R = _int32(y.numel() // K if K else 0, "rows of y")
+    _int32(T, "T"), _int32(pairs[1], "top_k"), _int32(K, "K")
     index = _device(y, "y")
     if out is None:
         out = torch.empty((T, K), dtype=torch.bfloat16 if residual is None else residual.dtype, device=y.device)
@@ -1076,8 +1091,7 @@ def moe_combine(y, rows, weights=None, residual=None, out=None):
     bits = _F32 if out_type else _BF16
     p = _pointers(index, ("y", "weights", "rows", "residual", "out"), y, _BF16, y.shape, weights, _F32, pairs, rows, _I32,
                   pairs, residual, bits, (T, K), out, bits, (T, K))
-    _call("dg_moe_combine", p[0], p[1], p[2], p[3], p[4], out_type, T, pairs[1], K, y.numel() // K if K else 0,
-          _raw_stream(index))
+    _call("dg_moe_combine", p[0], p[1], p[2], p[3], p[4], out_type, T, pairs[1], K, R, _raw_stream(index))
     return out
 
 

@@ -211,3 +211,22 @@ def test_binding():
         binding.layernorm_backward(x, x, workspace="none")
     with pytest.raises(binding.DGError, match="SHAPE"):
         binding.get_moe_rows(5, 2, 1025)
+
+
+def test_sizes_past_32_bits():
+    """Sizes whose low 32 bits would make a valid call are refused by name (tensors without memory)."""
+    import torch
+    n = (1 << 32) + 128
+    big = torch.empty((n, 8), dtype=torch.bfloat16, device="meta")
+    ids = torch.empty((n, 1), dtype=torch.int32, device="meta")
+    few = ids[:4]
+    for f, args in ((binding.layernorm_quantize_e4m3_1x128, (big,)), (binding.layernorm_backward, (big, big)),
+                    (binding.moe_sort_contiguous, (ids, 4)), (binding.moe_sort_masked, (ids, 4, 4)),
+                    (binding.moe_dispatch_quantize_e4m3_contiguous, (big, ids, 128)),
+                    (binding.moe_dispatch_quantize_e4m3_contiguous, (big[:4], few, n)),
+                    (binding.moe_dispatch_quantize_e4m3_masked, (big[:4], few, 4, n)),
+                    (binding.moe_dispatch_e4m3_contiguous, (big, big, ids, 128)),
+                    (binding.moe_combine, (big, few)), (binding.moe_combine, (big[:4], ids)),
+                    (binding.moe_combine_backward_quantize_e4m3_contiguous, (big[:4], big, few))):
+        with pytest.raises(ValueError, match="32 bits"):
+            f(*args)
