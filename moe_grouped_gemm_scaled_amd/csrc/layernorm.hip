@@ -16,7 +16,11 @@
 // would lose twice as many bits as |m| / spread has).
 //
 // Both are HBM-bound: a row is read once, held in registers between its
-// reductions and its outputs, and written once.
+// reductions and its outputs, and written once (4096 rows of 7168, bf16: 43.4 us,
+// 4.8 TB/s; 64 rows: 4.9 us; the gradient of 16384: 183 us, 5.1 TB/s, and 4.6 for
+// the sums of dw and db).  A second meeting of a row's waves for the variance
+// costs less than joining each wave's own mean and squared differences in one
+// (the gradient of 4096 rows 58.5 against 68.6 us).
 #include "dg_codes8.h"
 
 namespace dg {

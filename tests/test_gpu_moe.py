@@ -689,6 +689,31 @@ def test_rows_past_31_bits_of_offset():
         assert torch.equal(out[lo:lo + 128], (2 * block.float()).to(BF16)) and torch.equal(dw[lo:lo + 128], dw[:128])
 
 
+def test_sort_of_most_pairs():
+    """2^26 pairs, the most that the sort takes: every pair once, in order within its expert, behind the segment's start."""
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GiB of device memory")
+    T, k, G = 1 << 23, 8, 37
+    announce("sort of 2^26 pairs")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.randint(-1, G, (T, k), generator=g, device="cuda", dtype=I32)
+    rows, src, m, counts, ks = dg.moe_sort_contiguous(ids, G, src=True, counts=True, ks=True)
+    want = torch.zeros(G, dtype=torch.int64, device="cuda").index_add_(0, ids.view(-1).clamp_min(0).long(),
+                                                                       (ids.view(-1) >= 0).long())
+    assert torch.equal(counts.long(), want) and torch.equal(ks.long(), (want + 127) // 128 * 128)
+    flat, live = rows.view(-1), ids.view(-1) >= 0
+    assert torch.equal(flat >= 0, live)
+    pair = live.nonzero().flatten()
+    at = flat[pair].long()
+    assert torch.equal(src[at].long(), pair) and torch.equal(m[at], ids.view(-1)[pair])
+    assert int((src >= 0).sum()) == pair.numel() and torch.equal(src >= 0, m >= 0)
+    start = (ks.long().cumsum(0) - ks)[ids.view(-1)[pair].long()]
+    assert bool((at >= start).all()) and bool((at - start < want[ids.view(-1)[pair].long()]).all())
+    for e in range(G):                                 # in pair order
+        s = src[m == e]
+        assert bool((s[1:] > s[:-1]).all())
+
+
 # ---------------------------------------------------------------- the binding's refusals
 
 @pytest.fixture(params=["native", "python"])
