@@ -475,6 +475,8 @@ _BIT_TYPES = {_BF16: torch.bfloat16, _F32: torch.float32, _REAL: (torch.bfloat16
 # the current stream's handle without making a torch.cuda.Stream object (2.7 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+# the current device's index without the Python around it (0.2 us a call); a device tensor exists where it is asked for
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 try:
     from ._args import addresses as _native_addresses   # csrc/py_args.cpp: the checks of _raw, natively
@@ -503,7 +505,7 @@ def _device(t, name):
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{name}: must be a device tensor")
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         raise ValueError(f"{name}: on device {index}, but the current device is {torch.cuda.current_device()}")
     return index
 
@@ -811,7 +813,7 @@ def layernorm_quantize_e4m3_1x128(x, weight=None, bias=None, eps=1e-5, residual=
         raise ValueError("x: must have two dimensions, [rows, K]")
     shape = x.shape
     rows, K = shape
-    _int32(rows, "rows")
+    _fit_int32(("rows",), rows, 0)
     pitch, column = x.stride()
     if column != 1 and K > 1:
         raise ValueError("x: columns must be dense")
@@ -871,7 +873,7 @@ def layernorm_backward(dy, h, weight=None, eps=1e-5, dres=None, dx=None, dw=None
     if len(shape) != 2:
         raise ValueError(f"h: shape {tuple(shape)}, expected [rows, K]")
     rows, K = shape
-    _int32(rows, "rows")
+    _fit_int32(("rows",), rows, 0)
     if isinstance(workspace, str) and workspace != "auto":
         raise ValueError(f"workspace {workspace!r}")
     index = _device(h, "h")
@@ -910,11 +912,10 @@ def get_moe_sort_workspace_size(T: int, top_k: int, G: int) -> int:
     return int(v)
 
 
-def _int32(n, name):
-    """A size as the C call takes it: ctypes would drop the high bits of a larger one."""
-    if n > 0x7FFFFFFF:
-        raise ValueError(f"{name}: {n} does not fit 32 bits")
-    return n
+def _fit_int32(names, *sizes):
+    """Sizes as the C call takes them: ctypes would drop the high bits of a larger one."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(", ".join(f"{n}: {v} does not fit 32 bits" for n, v in zip(names, sizes) if v > 0x7FFFFFFF))
 
 
 def _sort_workspace(workspace, T, top_k, G, device):
@@ -936,7 +937,7 @@ def moe_sort_contiguous(ids, G, M_total=None, rows=None, src=None, m_indices=Non
     if ids.dim() != 2:
         raise ValueError("ids[T, top_k]")
     T, top_k = ids.shape
-    _int32(T, "T"), _int32(top_k, "top_k")
+    _fit_int32(("T", "top_k"), T, top_k)
     index = _device(ids, "ids")
     if M_total is None:
         M_total = get_moe_rows(T, top_k, G)
@@ -960,7 +961,7 @@ def moe_sort_masked(ids, G, M_cap, rows=None, src=None, masked_m=None, workspace
     if ids.dim() != 2:
         raise ValueError("ids[T, top_k]")
     T, top_k = ids.shape
-    _int32(T, "T"), _int32(top_k, "top_k")
+    _fit_int32(("T", "top_k"), T, top_k)
     index = _device(ids, "ids")
     i32, dev = torch.int32, ids.device
     if rows is None or masked_m is None or src is True:
@@ -987,7 +988,7 @@ def _dispatch(name, x, rows, lead, per, src, weights, y, q, sf, qt, sft, scales,
     if x.dim() != 2 or rows.dim() != 2:
         raise ValueError(f"{name}[T, K], rows[T, top_k]")
     T, K = x.shape
-    _int32(T, "T"), _int32(rows.shape[1], "top_k"), _int32(per, "rows")
+    _fit_int32(("T", "top_k", "rows"), T, rows.shape[1], per)
     pitch, column = x.stride()
     if column != 1 and K > 1:
         raise ValueError(f"{name}: columns must be dense")
@@ -1044,7 +1045,7 @@ def _dispatch_codes(q_in, sf_in, rows, lead, per, q, sf):
     if q_in.dim() != 2 or rows.dim() != 2 or sf_in.dim() != 2:
         raise ValueError("q_in[T, K], sf_in[K/128, ld], rows[T, top_k]")
     T, K = q_in.shape
-    _int32(T, "T"), _int32(rows.shape[1], "top_k"), _int32(per, "rows"), _int32(sf_in.shape[1], "ld")
+    _fit_int32(("T", "top_k", "rows", "ld"), T, rows.shape[1], per, sf_in.shape[1])
     index = _device(q_in, "q_in")
     packed = sf_in.dtype is torch.int32
     n, bits, ld = _sf_rows(packed, K // 128), _I32 if packed else _F32, (per + 3) // 4 * 4
@@ -1082,8 +1083,8 @@ def moe_combine(y, rows, weights=None, residual=None, out=None):
         raise ValueError("y[.., K], rows[T, top_k]")
     pairs = rows.shape
     T, K = pairs[0], y.shape[-1]
-    R = _int32(y.numel() // K if K else 0, "rows of y")
-    _int32(T, "T"), _int32(pairs[1], "top_k"), _int32(K, "K")
+    R = y.numel() // K if K else 0
+    _fit_int32(("T", "top_k", "K", "rows of y"), T, pairs[1], K, R)
     index = _device(y, "y")
     if out is None:
         out = torch.empty((T, K), dtype=torch.bfloat16 if residual is None else residual.dtype, device=y.device)
