@@ -90,6 +90,15 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(SortArgs p) {
     // workgroups past the last chunk rank nothing: they fill rows
     const int lo = min((int)blockIdx.x * p.chunk, p.n), hi = min(lo + p.chunk, p.n);
     const bool alone = gridDim.x == 1;
+    // the wave's run of pairs, on its way while the others are counted
+    constexpr int kMostRounds = 8;                     // chunk <= 8192
+    const int rounds = p.chunk / kSortThreads;
+    int key[kMostRounds];
+    static_for<kMostRounds>([&](auto rc) __attribute__((always_inline)) {
+        constexpr int r = decltype(rc)::value;
+        const int i = lo + (wave * rounds + r) * 64 + lane;
+        key[r] = r < rounds && i < hi ? p.ids[i] : -1;
+    });
     for (int e = t; e < 10 * G; e += kSortThreads) lds[e] = 0;
     __syncthreads();
     // ---- counts of the pairs before the chunk, and of those behind it
@@ -137,17 +146,13 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(SortArgs p) {
         __syncthreads();
     }
     // ---- ranks within the wave's run
-    constexpr int kMostRounds = 8;                     // chunk <= 8192
-    const int rounds = p.chunk / kSortThreads;
     const int bits = 32 - __clz(G);                    // keys 0 .. G, G: no expert
     uint16_t *mine = hist + wave * G;
-    int key[kMostRounds], rank[kMostRounds];
+    int rank[kMostRounds];
     static_for<kMostRounds>([&](auto rc) __attribute__((always_inline)) {
         constexpr int r = decltype(rc)::value;
         if (r < rounds) {                              // uniform
-            const int i = lo + (wave * rounds + r) * 64 + lane;
-            const int e = i < hi ? p.ids[i] : -1;
-            key[r] = (unsigned)e < (unsigned)G ? e : G;
+            key[r] = (unsigned)key[r] < (unsigned)G ? key[r] : G;
             const uint64_t m = same_key(key[r], bits);
             const int below = __popcll(m & ((1ull << lane) - 1));
             rank[r] = 0;
@@ -164,12 +169,13 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(SortArgs p) {
     // ---- the waves' counts become offsets; totals and padded sizes
     int32_t sum = 0;
     if (t < G) {
-        int run = 0;
+        int run = 0, c[kSortWaves];
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) c[w] = hist[w * G + t];     // all before the first is written
 #pragma unroll
         for (int w = 0; w < kSortWaves; ++w) {
-            const int c = hist[w * G + t];
             hist[w * G + t] = (uint16_t)run;
-            run += c;
+            run += c[w];
         }
         total[t] += before[t] + run;
         sum = p.cap ? 0 : (total[t] + 127) & ~127;
@@ -186,9 +192,11 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(SortArgs p) {
         }
         if (lane == 63) scan[wave] = inc;
         __syncthreads();
-        int base = 0;
-        for (int w = 0; w < wave; ++w) base += scan[w];
-        if (t < G) start[t] = base + inc - sum;
+        if (t < G) {
+            int base = 0;
+            for (int w = 0; w < wave; ++w) base += scan[w];
+            start[t] = base + inc - sum;
+        }
     }
     __syncthreads();
     auto room = [&](int e) __attribute__((always_inline)) { return p.cap ? p.cap : max(p.R - start[e], 0); };
@@ -251,13 +259,13 @@ static int sort_chunk(int64_t n) {
 }
 
 // Most pairs for which every workgroup counts all of them instead of a kernel
-// before it (32768 pairs, 64 experts: 8.0 us with the kernel before it, 9.8 without;
-// 16384 pairs: 7.5 without; each in a graph).
+// before it (32768 pairs, 64 experts: 8.0 us with the kernel before it, 9.3 without;
+// 16384 pairs: 7.1 without; each in a graph).
 constexpr int64_t kSortOneLaunch = 16384;
 
 // Workgroups: one per chunk, and one per 2048 rows of m_indices and src to
-// fill (512 pairs on 256 experts, 33024 rows: 5.9 us, 15.9 with one
-// workgroup; 1998 pairs on 32: 5.7, 6.6 with one).
+// fill (512 pairs on 256 experts, 33024 rows: 5.7 us, 15.9 with one
+// workgroup; 1998 pairs on 32: 5.3, 6.6 with one).
 constexpr int kSortFill = 2048;
 static int64_t sort_groups(int64_t n, int64_t R) {
     const int chunk = sort_chunk(n);
