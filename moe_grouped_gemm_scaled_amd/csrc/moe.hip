@@ -13,6 +13,7 @@
 //
 // Everything but the sort is HBM-bound.
 #include "dg_codes8.h"
+#include "dg_index.h"
 
 namespace dg {
 
@@ -223,11 +224,10 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(SortArgs p) {
     // ---- this workgroup's share of the rows: the expert of each, and -1 where there is none
     if (p.cap) {
         if (!p.src) return;
-        const int r_lo = (int)((int64_t)p.R * blockIdx.x / gridDim.x), r_hi = (int)((int64_t)p.R * (blockIdx.x + 1) / gridDim.x);
-        for (int r = r_lo + t; r < r_hi; r += kSortThreads) {
+        for_share(p.R, (int)blockIdx.x, (int)gridDim.x, t, kSortThreads, [&](int r) __attribute__((always_inline)) {
             const int e = r / p.cap;
             if (r - e * p.cap >= total[e]) p.src[r] = -1;
-        }
+        });
         return;
     }
     if (!p.src && !p.expert) return;

@@ -1,0 +1,52 @@
+"""GPU tests of the experts' row operators at the ends of their sizes."""
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from moe_grouped_gemm_scaled_amd import binding as dg
+
+pytestmark = pytest.mark.gpu
+BF16, I32 = torch.bfloat16, torch.int32
+
+
+def announce(msg):
+    print(f"\n[case] {msg}", file=sys.stderr, flush=True)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    dg.lib()
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
+def needs(gib):
+    if torch.cuda.mem_get_info()[0] < gib << 30:
+        pytest.skip(f"needs {gib} GiB of device memory")
+
+
+@pytest.mark.parametrize("G,cap", [(2, (1 << 30) - 1), (1, (1 << 31) - 1), (3, 715827882)])
+def test_masked_sort_into_the_most_rows(G, cap):
+    """G * M_cap just below 2^31: src holds the pairs and -1 elsewhere, and nothing is written around it."""
+    needs(16)
+    announce(f"masked sort into {G} x {cap} rows")
+    T, k, pad = 50, 3, 64
+    ids = np.random.default_rng(G).integers(-1, G + 1, (T, k)).astype(np.int32)
+    flat = torch.full((G * cap + 2 * pad,), 77, dtype=I32, device="cuda")
+    src = flat[pad:-pad].view(G, cap)
+    rows, got, masked_m = dg.moe_sort_masked(torch.from_numpy(ids).cuda(), G, cap, src=src)
+    torch.cuda.synchronize()
+    want_rows = np.full(T * k, -1, np.int64)
+    for e in range(G):
+        pairs = np.flatnonzero(ids.reshape(-1) == e)
+        want_rows[pairs] = e * cap + np.arange(pairs.size)
+        assert int(masked_m[e]) == pairs.size
+        assert np.array_equal(src[e, :pairs.size].cpu().numpy(), pairs)
+        assert bool((src[e, pairs.size:] == -1).all())
+    assert np.array_equal(rows.cpu().numpy().reshape(-1), want_rows)
+    assert bool((flat[:pad] == 77).all()) and bool((flat[-pad:] == 77).all())
