@@ -16,4 +16,15 @@ __host__ __device__ __forceinline__ void for_share(int n, int part, int parts, i
     for (uint32_t i = lo + (uint32_t)t; i < hi; i += (uint32_t)step) f((int)i);
 }
 
+// Part `part` of [0, n) dealt to `parts`: [lo, hi).  The first n % parts of them
+// take one more; no product passes n.
+struct Share {
+    int lo, hi;
+};
+__host__ __device__ __forceinline__ Share share_of(int n, int part, int parts) {
+    const int each = n / parts, more = n - each * parts;
+    const int lo = each * part + (part < more ? part : more);
+    return {lo, lo + each + (part < more ? 1 : 0)};
+}
+
 }  // namespace dg

@@ -377,7 +377,8 @@ moe_dispatch_kernel(DispatchArgs p) {
     const int w0 = WPR == 1 ? 0 : wave;
     const int K = p.K;
     if (WPR == 1 && tok >= p.T) return;
-    const int j_lo = p.top_k * (int)blockIdx.y / (int)gridDim.y, j_hi = p.top_k * ((int)blockIdx.y + 1) / (int)gridDim.y;
+    const Share choices = share_of(p.top_k, (int)blockIdx.y, (int)gridDim.y);
+    const int j_lo = choices.lo, j_hi = choices.hi;
     const int32_t *rows = p.rows + (int64_t)tok * p.top_k;
     const float *ws = kW ? p.weights + (int64_t)tok * p.top_k : nullptr;
 

@@ -48,9 +48,26 @@ static int test_for_share() {
     return 0;
 }
 
+static int test_share_of() {
+    for (int n : {0, 1, 7, 8, 255, 256, 257, 1000, (1 << 23) - 1, 1 << 23, 1 << 24, (1 << 26) - 1, 1 << 26, 1 << 30, INT32_MAX}) {
+        for (int parts : {1, 2, 5, 255, 256, 304, 1024}) {
+            int at = 0;
+            for (int part = 0; part < parts; ++part) {
+                const dg::Share s = dg::share_of(n, part, parts);
+                CHECK(s.lo == at);
+                CHECK(s.hi - s.lo - n / parts == 0 || s.hi - s.lo - n / parts == 1);
+                at = s.hi;
+            }
+            CHECK(at == n);
+        }
+    }
+    return 0;
+}
+
 int main(int argc, char **argv) {
     const char *what = argc > 1 ? argv[1] : "";
     if (!strcmp(what, "for_share")) test_for_share();
+    else if (!strcmp(what, "share_of")) test_share_of();
     else return 2;
     if (!failures) printf("ok: %s\n", what);
     return failures != 0;

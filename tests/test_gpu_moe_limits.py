@@ -50,3 +50,31 @@ def test_masked_sort_into_the_most_rows(G, cap):
         assert bool((src[e, pairs.size:] == -1).all())
     assert np.array_equal(rows.cpu().numpy().reshape(-1), want_rows)
     assert bool((flat[:pad] == 77).all()) and bool((flat[-pad:] == 77).all())
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+def test_dispatch_of_a_token_with_many_choices(weighted):
+    """One token with 2^24 choices, dealt to as many workgroups as there are CUs: every row holds it, and every weight has
+    its gradient."""
+    needs(24)
+    k, K = (1 << 24) + 5, 128
+    announce(f"dispatch of one token with {k} choices weighted={weighted}")
+    x = torch.linspace(-3, 3, K, device="cuda").to(BF16).view(1, K)
+    R = (k + 127) // 128 * 128
+    # backwards, so that a choice's row tells its place
+    rows = torch.arange(k - 1, -1, -1, dtype=I32, device="cuda").view(1, k)
+    w = (1 + (torch.arange(k, device="cuda") % 7)).view(1, k).float() if weighted else None
+    q, sf, _, _, _ = dg.moe_dispatch_quantize_e4m3_contiguous(x, rows, R, weights=w)
+    values = x.float() * (torch.arange(1, 8, device="cuda").view(7, 1) if weighted else torch.ones(7, 1, device="cuda"))
+    wq, wsf = dg.quantize_e4m3_1x128(values.contiguous())
+    at = (k - 1 - torch.arange(k, device="cuda")) % 7                  # of the choice in each row
+    for lo in range(0, k, 1 << 20):
+        part = at[lo:lo + (1 << 20)]
+        assert torch.equal(q[lo:lo + part.numel()], wq[part])
+        assert torch.equal(sf[0, lo:lo + part.numel()], wsf[0, part])
+    assert not q[k:].any() and not sf[0, k:].any()
+    del q, sf
+    ye = torch.zeros((R, K), dtype=BF16, device="cuda")
+    ye[:k, 0] = (1 + torch.arange(k, device="cuda") % 5).to(BF16)      # exact products: -3 * 1 .. 5
+    dw, *_ = dg.moe_combine_backward_quantize_e4m3_contiguous(x, ye, rows, w, dw=True)
+    assert torch.equal(dw.view(-1), x[0, 0].float() * ye[:k, 0].float().flip(0))

@@ -34,3 +34,8 @@ def run(driver, what):
 def test_shares_of_the_most_rows(driver):
     """A workgroup's share of a layout's rows, where the step past its last row reaches 2^31."""
     run(driver, "for_share")
+
+
+def test_shares_of_the_most_choices(driver):
+    """A workgroup's share of a token's choices, up to as many as a call may have."""
+    run(driver, "share_of")
