@@ -27,4 +27,7 @@ __host__ __device__ __forceinline__ Share share_of(int n, int part, int parts) {
     return {lo, lo + each + (part < more ? 1 : 0)};
 }
 
+// Runs of `size` that cover n (n + size may pass 2^31).
+__host__ __device__ __forceinline__ int runs_of(int n, int size) { return n / size + (n % size != 0); }
+
 }  // namespace dg

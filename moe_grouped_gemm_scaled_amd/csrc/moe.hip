@@ -1057,7 +1057,7 @@ hipError_t launch_moe_combine(const MoeCombineProblem &p, hipStream_t stream) {
                                static_cast<float *>(p.out), n8);
         return hipGetLastError();
     }
-    const int chunks = (p.K + 511) / 512;
+    const int chunks = runs_of(p.K, 512);
     const CombineArgs a{p.y, p.weights, p.rows, p.residual, p.out, p.T, p.top_k, p.K, p.R, chunks, Divisor(chunks)};
     return p.out_type == kBf16 ? launch_combine_t<uint16_t>(a, stream) : launch_combine_t<float>(a, stream);
 }

@@ -64,10 +64,21 @@ static int test_share_of() {
     return 0;
 }
 
+static int test_runs_of() {
+    for (int n : {0, 8, 504, 512, 520, 1024, 16384, 1 << 30, INT32_MAX - 519, INT32_MAX - 511, INT32_MAX - 510, INT32_MAX - 7}) {
+        const int64_t runs = dg::runs_of(n, 512);
+        CHECK(runs * 512 >= n && (runs - 1) * 512 < n);
+        // the columns of the last run's last lane still fit an int
+        CHECK((runs - 1) * 512 + 8 * 63 <= INT32_MAX);
+    }
+    return 0;
+}
+
 int main(int argc, char **argv) {
     const char *what = argc > 1 ? argv[1] : "";
     if (!strcmp(what, "for_share")) test_for_share();
     else if (!strcmp(what, "share_of")) test_share_of();
+    else if (!strcmp(what, "runs_of")) test_runs_of();
     else return 2;
     if (!failures) printf("ok: %s\n", what);
     return failures != 0;

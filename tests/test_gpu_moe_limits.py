@@ -78,3 +78,20 @@ def test_dispatch_of_a_token_with_many_choices(weighted):
     ye[:k, 0] = (1 + torch.arange(k, device="cuda") % 5).to(BF16)      # exact products: -3 * 1 .. 5
     dw, *_ = dg.moe_combine_backward_quantize_e4m3_contiguous(x, ye, rows, w, dw=True)
     assert torch.equal(dw.view(-1), x[0, 0].float() * ye[:k, 0].float().flip(0))
+
+
+@pytest.mark.parametrize("K", [(1 << 31) - 8, (1 << 31) - 512, 1 << 30])
+def test_combine_of_the_widest_rows(K):
+    """Rows of up to 2^31 - 8 columns: the last columns come out as the first, and nothing is written past them."""
+    needs(24)
+    announce(f"combine K={K}")
+    flat = torch.full((K + 128,), 7.0, dtype=BF16, device="cuda")
+    out, y = flat[64:-64].view(1, K), torch.empty((1, K), dtype=BF16, device="cuda")
+    y.view(-1, 8).copy_(torch.arange(8, device="cuda").to(BF16))
+    y[0, -8:] += 8
+    rows = torch.tensor([[0, -1]], dtype=I32, device="cuda")
+    dg.moe_combine(y, rows, weights=torch.tensor([[2.0, 5.0]], device="cuda"), out=out)
+    torch.cuda.synchronize()
+    y.mul_(2)
+    assert torch.equal(out, y)
+    assert bool((flat[:64] == 7).all()) and bool((flat[-64:] == 7).all())

@@ -39,3 +39,8 @@ def test_shares_of_the_most_rows(driver):
 def test_shares_of_the_most_choices(driver):
     """A workgroup's share of a token's choices, up to as many as a call may have."""
     run(driver, "share_of")
+
+
+def test_runs_of_the_widest_rows(driver):
+    """512-column runs of a row, up to the widest that combine takes."""
+    run(driver, "runs_of")
