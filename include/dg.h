@@ -731,8 +731,8 @@ int64_t dg_get_moe_sort_workspace_size(int T, int top_k, int G);
  *       dg_k_grouped_fp8_gemm_tn_contiguous (for the weight gradient); needs src
  *       (the sort's, of the same rows)
  * Errors: DG_ERR_NULL; DG_ERR_SHAPE (T < 0; top_k, G, M_cap < 1; M_total < 0 or
- * % 128; K < 128, K % 128, K > 16384; T * top_k or the rows reaching 2^31);
- * DG_ERR_ARG (x_type); DG_ERR_ALIGN.
+ * % 128; K < 128, K % 128, K > 16384; top_k > 2^30; T * top_k or the rows
+ * reaching 2^31); DG_ERR_ARG (x_type); DG_ERR_ALIGN.
  */
 int dg_moe_dispatch_quantize_e4m3_contiguous(const void *x, int x_type, int64_t ld_x, const float *weights,
                                              const int32_t *rows, const int32_t *src,
@@ -785,8 +785,8 @@ int dg_moe_dispatch_e4m3_masked_ue8m0_packed(const uint8_t *q_in, const uint32_t
  *                          weights)
  *   residual, out [T][K]   out_type DG_BF16 or DG_F32; residual NULL = 0, and
  *                          may be out (in place)
- * Errors: DG_ERR_NULL; DG_ERR_SHAPE (T, R < 0; top_k < 1; K < 8 or K % 8;
- * T * top_k reaching 2^31); DG_ERR_ARG (out_type); DG_ERR_ALIGN.
+ * Errors: DG_ERR_NULL; DG_ERR_SHAPE (T, R < 0; top_k < 1 or > 2^30; K < 8 or
+ * K % 8; T * top_k reaching 2^31); DG_ERR_ARG (out_type); DG_ERR_ALIGN.
  */
 int dg_moe_combine(const uint16_t *y, const float *weights, const int32_t *rows, const void *residual,
                    void *out, int out_type, int T, int top_k, int K, int R, void *stream);

@@ -41,10 +41,12 @@ int layernorm_impl(const void *x, int x_type, int64_t ld_x, const void *residual
     return status(dg::launch_layernorm_quant(p, static_cast<hipStream_t>(stream)));
 }
 
-// Pairs of T tokens, or -1 where they reach 2^31.
+// Pairs of T tokens, or -1 where they reach 2^31 or a token's choices pass 2^30:
+// kernels walk these in steps of up to 64 and hold the next step's start in an int.
+constexpr int kMaxTopK = 1 << 30;
 int64_t moe_pairs(int T, int top_k) {
     const int64_t n = (int64_t)T * top_k;
-    return T < 0 || top_k < 1 || n >= kIndexLimit ? -1 : n;
+    return T < 0 || top_k < 1 || top_k > kMaxTopK || n >= kIndexLimit ? -1 : n;
 }
 
 bool moe_sort_sizes(int64_t n, int G) { return n >= 0 && n <= dg::kMoeMaxPairs && G >= 1 && G <= dg::kMoeMaxExperts; }
