@@ -796,6 +796,13 @@ def gated_backward_quantize_e4m3(gu, dh, act="silu", m_indices=None, dgu=None, q
     return dgu, q, sf, qt, sft, ht, sfht
 
 
+def _fit_int32(names, *sizes):
+    """Sizes as the C call takes them: ctypes would drop the high bits of what 32 do not hold."""
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+        raise ValueError(", ".join(f"{n}: {v} does not fit 32 bits" for n, v in zip(names, sizes)
+                                   if not -0x80000000 <= v <= 0x7FFFFFFF))
+
+
 _LN_NAMES = ("residual", "weight", "bias", "residual_out", "y", "q", "sf")
 
 
@@ -813,7 +820,7 @@ def layernorm_quantize_e4m3_1x128(x, weight=None, bias=None, eps=1e-5, residual=
         raise ValueError("x: must have two dimensions, [rows, K]")
     shape = x.shape
     rows, K = shape
-    _fit_int32(("rows",), rows, 0)
+    _fit_int32(("rows", "K", "ld_sf"), rows, K, ld_sf if ld_sf is not None else 0 if sf is None else sf.shape[-1])
     pitch, column = x.stride()
     if column != 1 and K > 1:
         raise ValueError("x: columns must be dense")
@@ -854,7 +861,9 @@ def layernorm_quantize_e4m3_1x128(x, weight=None, bias=None, eps=1e-5, residual=
 
 def get_layernorm_backward_workspace_size(rows: int, K: int) -> int:
     """Bytes of scratch layernorm_backward needs on the current device (of any content)."""
-    v = lib().dg_get_layernorm_backward_workspace_size(int(rows), int(K))
+    rows, K = int(rows), int(K)
+    _fit_int32(("rows", "K"), rows, K)
+    v = lib().dg_get_layernorm_backward_workspace_size(rows, K)
     if v < 0:
         raise DGError(int(v), "dg_get_layernorm_backward_workspace_size")
     return int(v)
@@ -873,7 +882,7 @@ def layernorm_backward(dy, h, weight=None, eps=1e-5, dres=None, dx=None, dw=None
     if len(shape) != 2:
         raise ValueError(f"h: shape {tuple(shape)}, expected [rows, K]")
     rows, K = shape
-    _fit_int32(("rows",), rows, 0)
+    _fit_int32(("rows", "K"), rows, K)
     if isinstance(workspace, str) and workspace != "auto":
         raise ValueError(f"workspace {workspace!r}")
     index = _device(h, "h")
@@ -898,7 +907,9 @@ def layernorm_backward(dy, h, weight=None, eps=1e-5, dres=None, dx=None, dw=None
 
 def get_moe_rows(T: int, top_k: int, G: int) -> int:
     """Rows of the contiguous layout that hold T * top_k pairs however they fall on G experts (dg_get_moe_rows)."""
-    v = lib().dg_get_moe_rows(int(T), int(top_k), int(G))
+    T, top_k, G = int(T), int(top_k), int(G)
+    _fit_int32(("T", "top_k", "G"), T, top_k, G)
+    v = lib().dg_get_moe_rows(T, top_k, G)
     if v < 0:
         raise DGError(int(v), "dg_get_moe_rows")
     return int(v)
@@ -906,16 +917,12 @@ def get_moe_rows(T: int, top_k: int, G: int) -> int:
 
 def get_moe_sort_workspace_size(T: int, top_k: int, G: int) -> int:
     """Bytes of scratch (of any content) that the sort of T * top_k pairs uses (0: none)."""
-    v = lib().dg_get_moe_sort_workspace_size(int(T), int(top_k), int(G))
+    T, top_k, G = int(T), int(top_k), int(G)
+    _fit_int32(("T", "top_k", "G"), T, top_k, G)
+    v = lib().dg_get_moe_sort_workspace_size(T, top_k, G)
     if v < 0:
         raise DGError(int(v), "dg_get_moe_sort_workspace_size")
     return int(v)
-
-
-def _fit_int32(names, *sizes):
-    """Sizes as the C call takes them: ctypes would drop the high bits of a larger one."""
-    if max(sizes) > 0x7FFFFFFF:
-        raise ValueError(", ".join(f"{n}: {v} does not fit 32 bits" for n, v in zip(names, sizes) if v > 0x7FFFFFFF))
 
 
 def _sort_workspace(workspace, T, top_k, G, device):
@@ -937,7 +944,7 @@ def moe_sort_contiguous(ids, G, M_total=None, rows=None, src=None, m_indices=Non
     if ids.dim() != 2:
         raise ValueError("ids[T, top_k]")
     T, top_k = ids.shape
-    _fit_int32(("T", "top_k"), T, top_k)
+    _fit_int32(("T", "top_k", "G", "M_total"), T, top_k, G, 0 if M_total is None else M_total)
     index = _device(ids, "ids")
     if M_total is None:
         M_total = get_moe_rows(T, top_k, G)
@@ -961,7 +968,7 @@ def moe_sort_masked(ids, G, M_cap, rows=None, src=None, masked_m=None, workspace
     if ids.dim() != 2:
         raise ValueError("ids[T, top_k]")
     T, top_k = ids.shape
-    _fit_int32(("T", "top_k"), T, top_k)
+    _fit_int32(("T", "top_k", "G", "M_cap"), T, top_k, G, M_cap)
     index = _device(ids, "ids")
     i32, dev = torch.int32, ids.device
     if rows is None or masked_m is None or src is True:
@@ -988,7 +995,7 @@ def _dispatch(name, x, rows, lead, per, src, weights, y, q, sf, qt, sft, scales,
     if x.dim() != 2 or rows.dim() != 2:
         raise ValueError(f"{name}[T, K], rows[T, top_k]")
     T, K = x.shape
-    _fit_int32(("T", "top_k", "rows"), T, rows.shape[1], per)
+    _fit_int32(("T", "top_k", "K", "rows", "G"), T, rows.shape[1], K, per, *lead)
     pitch, column = x.stride()
     if column != 1 and K > 1:
         raise ValueError(f"{name}: columns must be dense")
@@ -1045,7 +1052,7 @@ def _dispatch_codes(q_in, sf_in, rows, lead, per, q, sf):
     if q_in.dim() != 2 or rows.dim() != 2 or sf_in.dim() != 2:
         raise ValueError("q_in[T, K], sf_in[K/128, ld], rows[T, top_k]")
     T, K = q_in.shape
-    _fit_int32(("T", "top_k", "rows", "ld"), T, rows.shape[1], per, sf_in.shape[1])
+    _fit_int32(("T", "top_k", "K", "rows", "ld", "G"), T, rows.shape[1], K, per, sf_in.shape[1], *lead)
     index = _device(q_in, "q_in")
     packed = sf_in.dtype is torch.int32
     n, bits, ld = _sf_rows(packed, K // 128), _I32 if packed else _F32, (per + 3) // 4 * 4
