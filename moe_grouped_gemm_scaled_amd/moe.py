@@ -63,10 +63,10 @@ class MoEFFN:
         ids, w = self._route(n)
         rows, src, m_indices, _, ks = dg.moe_sort_contiguous(ids, self.G, src=True if save else None, ks=True if save else None)
         R = m_indices.shape[0]
-        if save:
-            nq, sfn, nqt, sfnt, _ = dg.moe_dispatch_quantize_e4m3_contiguous(n, rows, R, src=src, q=True, qt=True)
-        else:
-            nq, sfn = dg.moe_dispatch_e4m3_contiguous(q, sf, rows, R)
+        # the norm's own codes, of n before its rounding to bf16, whether or not a backward pass follows
+        nq, sfn = dg.moe_dispatch_e4m3_contiguous(q, sf, rows, R)
+        if save:                                       # n along columns too, for the weight gradient
+            _, _, nqt, sfnt, _ = dg.moe_dispatch_quantize_e4m3_contiguous(n, rows, R, src=src, q=False, qt=True)
         _, a, sfa, gu = dg.m_grouped_fp8_gated_gemm_nt_contiguous(nq, sfn, self.gu, self.sf_gu, m_indices, act=self.act, q=True,
                                                                   gu=True if save else None)
         y = torch.empty((R, self.H), dtype=bf16, device=dev)
