@@ -624,7 +624,8 @@ int dg_gated_backward_quantize_e4m3_ue8m0(const uint16_t *gu, const uint16_t *dh
  * The mean is subtracted before the squares are summed, so a mean that is large
  * beside the spread costs no more bits than h itself holds.  Sums of squares
  * overflow fp32 for differences above about 1e19: v is then infinite and y the
- * bias.  A row with an infinity or NaN in it is NaN throughout (codes 0x7f).
+ * bias.  A row with an infinity or NaN in it is NaN throughout (codes 0x7f); so
+ * is a row whose sum passes fp32, and with eps = 0 a row of equal values.
  * Errors as there.
  */
 int dg_layernorm_quantize_e4m3_1x128(const void *x, int x_type, int64_t ld_x,
