@@ -652,6 +652,7 @@ int dg_layernorm_quantize_e4m3_1x128_ue8m0_packed(const void *x, int x_type, int
  * where there is no residual); the quantisation is taken as the identity.
  *   r = 1 / sqrt(v + eps),  n = (h - m) * r,  g = dy * weight
  *   dx = dres + r * (g - mean_k(g) - n * mean_k(g * n))   [rows][K], h's type
+ *                     (r^2 is formed: v + eps above 2.9e-39)
  *   dw = sum over rows of dy * n,  db = sum over rows of dy   [K] fp32, each optional
  * weight, dres optional; the rest as for dg_rmsnorm_backward, K a multiple of 8.
  *   workspace: dg_get_layernorm_backward_workspace_size(rows, K) bytes of

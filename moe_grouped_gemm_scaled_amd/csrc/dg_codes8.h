@@ -1,6 +1,6 @@
 // dg_codes8.h -- 1x128 quantisation of eight consecutive columns per lane, 16
-// lanes to a block, four blocks (one packed scale word) to a wave: what the
-// row-wise kernels that write E4M3 rows share.
+// lanes to a block, four blocks (one packed scale word) to a wave: how the layer
+// norm writes its rows.
 #pragma once
 
 #include "dg_layer.h"

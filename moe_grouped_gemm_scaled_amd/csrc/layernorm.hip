@@ -15,10 +15,11 @@
 // nothing cancels where the mean is large beside the spread (mean(h^2) - m^2
 // would lose twice as many bits as |m| / spread has).
 //
-// Both are HBM-bound: a row is read once, held in registers between its
-// reductions and its outputs, and written once (4096 rows of 7168, bf16: 43.4 us,
+// A row is read once, held in registers between its reductions and its outputs,
+// and written once, so that HBM bounds both (4096 rows of 7168, bf16: 43.4 us,
 // 4.8 TB/s; 64 rows: 4.9 us; the gradient of 16384: 183 us, 5.1 TB/s, and 4.6 for
-// the sums of dw and db).  A second meeting of a row's waves for the variance
+// the sums of dw and db), except the gradient of more than 4096 columns with fp32
+// h or dy, whose registers do not suffice (LnBwdShape).  A second meeting of a row's waves for the variance
 // costs less than joining each wave's own mean and squared differences in one
 // (the gradient of 4096 rows 58.5 against 68.6 us).
 #include "dg_codes8.h"
@@ -191,7 +192,11 @@ static hipError_t launch_fwd_t(const LnFwdArgs &a, hipStream_t stream) {
 
 // Waves per row, as in the RMS norm, whose traffic is the same: one up to 1024
 // columns, four from there, sixteen for few long rows, where a row's latency is
-// the call's.
+// the call's.  Calls among others, bf16 with residual, the RMS norm's beside them:
+// 64 x 7168 6.7 us (6.2), 4096 x 1024 7.6 (7.2), x 4096 24.1 (24.4), x 7168 41.3
+// (40.6), 2048 x 16384 51.8 (51.6).  Lanes are dealt columns in powers of two, so
+// just past a step nearly half of them count as nothing: 4096 x 1152 10.8 us, 3.1
+// TB/s (9.4), x 2176 15.5, 4.1 TB/s (14.5), x 4224 27.9, 4.4 TB/s (26.1).
 template <typename TX, typename TR, typename TW>
 static hipError_t launch_fwd_k(const LnFwdArgs &a, hipStream_t stream) {
     const int n = (a.K + 511) / 512;                   // 512-column chunks
@@ -243,6 +248,10 @@ struct LnBwdArgs {
 // two such workgroups per CU where a thread holds 8 columns: 16384 rows of 2048:
 // 63.0, 76.5 with four waves, 82 with one workgroup; sixteen waves: 60.6 there,
 // but 9.9 against 8.7 for 333 rows.
+// With fp32 h or dy and four chunks per lane the 256 registers do not hold all of
+// it: 17 to 68 are spilled to scratch.  4096 rows of 7168 take 89 us with fp32 dy,
+// 137 with fp32 h and 185 with both (3.3 to 2.5 TB/s), 56 with neither; up to 4096
+// columns nothing is spilled (4096 rows of 4096: 41, 54 and 62 us, 4.1 to 4.4 TB/s).
 template <int WPR, int NCH>
 struct LnBwdShape {
     static constexpr int kThreads = 512;

@@ -12,8 +12,10 @@
 // (and combine without weights is the gradient of dispatch).
 //
 // Everything but the sort is HBM-bound.
-#include "dg_codes8.h"
 #include "dg_index.h"
+#include "dg_layer.h"
+#include "dg_quant.h"
+#include "dg_rows.h"
 
 namespace dg {
 
@@ -260,7 +262,11 @@ static int sort_chunk(int64_t n) {
 
 // Most pairs for which every workgroup counts all of them instead of a kernel
 // before it (32768 pairs, 64 experts: 8.0 us with the kernel before it, 9.3 without;
-// 16384 pairs: 7.1 without; each in a graph).
+// 16384 pairs: 7.1 without; each in a graph).  The table of counts has a row per
+// chunk, and every workgroup reads all of it: chunks grow to 8192 pairs, and past
+// 2^19 pairs the reads grow with the square of the pairs (in a graph, 64 experts:
+// 2^19 pairs 22 us, 2^23 100, 2^26 1.9 ms; 1024 experts: 2^20 44 us, 2^23 454, 2^26
+// 22 ms).
 constexpr int64_t kSortOneLaunch = 16384;
 
 // Workgroups: one per chunk, and one per 2048 rows of m_indices and src to
@@ -365,7 +371,8 @@ __device__ __forceinline__ float sum_of_runs(const float *d, int runs) {
 // Bound by the stores: 4096 tokens of 7168 to 8 rows each 62 to 65 us, 3.8 TB/s of
 // codes (76 with 8 columns per lane and every row and scale looked up and stored
 // per chunk; 68 of those without the scales); one token to 8 rows 3.7 us, 5.5 from
-// a single workgroup.
+// a single workgroup.  With weights a token is encoded once per choice: 79 us, and
+// with the dot products, which read the experts' rows, 149 (5.2 TB/s in all).
 // kDot: also dw[t, j] = x[t] . ye[rows[t, j]], added up in a fixed order.
 template <typename TX, int WPR, int NCH, bool kW, bool kDot>
 __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR)
@@ -540,6 +547,12 @@ static hipError_t launch_dispatch_t(const DispatchArgs &a, int num_cus, hipStrea
     return hipGetLastError();
 }
 
+// Waves per token, 16 columns of each lane's where they reach; two runs of columns
+// per lane from 4097 columns on, but eight waves for fewer than 512 tokens, where a
+// token's latency shows and each wave encodes half as much per choice (in a graph,
+// 8 choices, 7168 columns: 500 tokens 8.9 us, 9.7 with four waves, with weights 13.6
+// and 14.6; 64 tokens with weights 4.7 and 5.4; 1024 tokens 16.8, 17.5 with eight, of
+// 4224 columns 10.4 and 12.6).
 template <typename TX, bool kW, bool kDot>
 static hipError_t launch_dispatch_k(const DispatchArgs &a, int num_cus, hipStream_t stream) {
     const int n = (a.K + 1023) / 1024;                 // 1024-column chunks
@@ -965,7 +978,9 @@ struct CombineArgs {
 // in flight together: a choice without a row reads row 0 (and counts as nothing),
 // since a load under a condition waits for the one before it (64 tokens of 7168,
 // 8 choices: 4.3 us, 6.9 so).  Four of them: 4096 tokens 103.6 us in a graph, 4.6
-// TB/s of rows; all 8 at once, 103.5, and 4.6 for the 64.  Workgroups in launch
+// TB/s of rows; all 8 at once, 103.5, and 4.6 for the 64.  Two for one or two
+// choices (4096 tokens of 7168, one choice: 30.6 us, 35.1 with four, two choices:
+// 39.0 and 40.2; 333 of 2048: 3.2 and 3.5, 3.3 and 3.7).  Workgroups in launch
 // order: 112 us with neighbours on one XCD.  The sum runs in the order of the
 // choices, in fp32.
 template <typename TO, bool kRes, bool kW, int kBatch>
